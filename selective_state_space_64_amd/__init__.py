@@ -1,8 +1,8 @@
 """Selective state-space (S6) scan for AMD MI355X (gfx950).
 
-Thin Python binding over the C ABI in ``include/ssm.h``, ``include/ssm_bwd.h``
-and ``include/ssm_conv.h`` (``libssm.so``):
-argument marshalling only.  Every step of the computation runs in the HIP
+Thin Python binding over the C ABI in ``include/ssm.h``, ``include/ssm_bwd.h``,
+``include/ssm_conv.h``, ``include/ssm_delta.h`` and ``include/ssm_norm.h``
+(``libssm.so``): argument marshalling only.  Every step of the computation runs in the HIP
 kernels of ``csrc/``; PyTorch only provides device memory and the stream.
 There is no CPU fallback: if the library is missing or no GPU is present the
 calls raise.
@@ -12,10 +12,18 @@ calls raise.
     grads = ssm_scan_bwd(x, dt, A, Bm, Cm, dy, dt_bias=..., Dskip=..., z=..., h0=..., dhL=...)
     y, stateL = ssm_conv1d_fwd(x, weight, bias=..., state0=..., silu=True)
     y = ssm_conv1d_update(state, x, weight, bias=..., silu=True)
+    y, hL = ssm_delta_fwd(q, k, v, g, beta, scale=..., h0=..., cu_seqlens=...)
+    grads = ssm_delta_bwd(q, k, v, g, beta, dy, scale=..., h0=..., dhL=..., cu_seqlens=...)
+    y = ssm_delta_update(state, q, k, v, g, beta, scale=..., slots=...)
+    y = ssm_group_norm_fwd(x, groups, weight=..., bias=..., z=..., rms=..., silu=...)
+    grads = ssm_group_norm_bwd(x, groups, dy, weight=..., bias=..., z=...)
 
 Layouts: x, dt, z, y [batch, dim, L]; Bm, Cm [batch, N, L]; A [dim, N];
 Dskip, dt_bias [dim]; h0, hL, state [batch, dim, N] (decode: drop L);
 conv weight [dim, W], bias [dim], conv state [batch, dim, W-1].
+Gated delta rule: q, k [batch, L, qk_heads, K]; v, y [batch, L, heads, V];
+g, beta [batch, L, heads]; states [sequences, heads, K, V] (decode: drop L).
+Grouped norm: x, z, y [batch, L, dim] or [batch, dim].
 """
 import ctypes
 import functools
@@ -30,6 +38,7 @@ SSM_F32, SSM_BF16 = 0, 1
 SSM_FLAG_ZOH_B = 0x1
 SSM_FLAG_CHECKPOINTS = 0x2
 SSM_CONV_SILU = 0x1
+SSM_NORM_RMS, SSM_NORM_SILU, SSM_NORM_GATE_FIRST = 0x1, 0x2, 0x4
 STATUS = {
     0: "SSM_OK", 1: "SSM_ERR_NULL_ARG", 2: "SSM_ERR_BAD_SHAPE", 3: "SSM_ERR_BAD_DTYPE",
     4: "SSM_ERR_MISALIGNED", 5: "SSM_ERR_ALIAS", 6: "SSM_ERR_UNSUPPORTED",
@@ -42,7 +51,10 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_fwd_workspace_bytes
            "ssm_conv1d_fwd", "ssm_conv1d_fwd_strided", "ssm_conv1d_fwd_bld", "ssm_conv1d_update",
            "ssm_conv1d_update_strided",
            "ssm_scan_bwd_workspace_bytes", "ssm_scan_bwd", "ssm_scan_bwd_strided",
-           "ssm_scan_bwd_bld_workspace_bytes", "ssm_scan_bwd_bld"]
+           "ssm_scan_bwd_bld_workspace_bytes", "ssm_scan_bwd_bld",
+           "ssm_delta_fwd_workspace_bytes", "ssm_delta_fwd",
+           "ssm_delta_bwd_workspace_bytes", "ssm_delta_bwd", "ssm_delta_update",
+           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_bytes", "ssm_group_norm_bwd"]
 
 
 class ScanLayout(ctypes.Structure):
@@ -88,6 +100,27 @@ class UpdateLayout(ctypes.Structure):
     _fields_ = [("x_batch", ctypes.c_longlong), ("dt_batch", ctypes.c_longlong),
                 ("z_batch", ctypes.c_longlong), ("y_batch", ctypes.c_longlong),
                 ("B_batch", ctypes.c_longlong), ("C_batch", ctypes.c_longlong)]
+
+
+class DeltaLayout(ctypes.Structure):
+    """ssm_delta_layout_t: step, head and batch strides in elements of q, k, v,
+    y, g, beta, 0 = dense default."""
+    _fields_ = [(n, ctypes.c_longlong * 6) for n in ("step", "head", "batch")]
+
+
+class DeltaBwdLayout(ctypes.Structure):
+    """ssm_delta_bwd_layout_t: the same for q, k, v, g, beta, dy, dq, dk, dv."""
+    _fields_ = [(n, ctypes.c_longlong * 9) for n in ("step", "head", "batch")]
+
+
+class NormLayout(ctypes.Structure):
+    """ssm_norm_layout_t: step and batch strides of x, z, y, 0 = dense default."""
+    _fields_ = [(n, ctypes.c_longlong * 3) for n in ("step", "batch")]
+
+
+class NormBwdLayout(ctypes.Structure):
+    """ssm_norm_bwd_layout_t: the same for x, z, dy, dx, dz."""
+    _fields_ = [(n, ctypes.c_longlong * 5) for n in ("step", "batch")]
 
 
 class SSMError(RuntimeError):
@@ -157,6 +190,21 @@ def lib():
                                          [i, vp, vp, ctypes.POINTER(ConvBldLayout), vp])
         L.ssm_conv1d_update.restype = i
         L.ssm_conv1d_update.argtypes = [i, i, i, i, u] + [vp] * 4 + [i, vp, vp]
+        for name in ("ssm_delta_fwd_workspace_bytes", "ssm_delta_bwd_workspace_bytes"):
+            getattr(L, name).restype = sz
+            getattr(L, name).argtypes = [i] * 7
+        L.ssm_delta_fwd.restype = i
+        L.ssm_delta_fwd.argtypes = [i] * 7 + [u, vp] + [vp] * 7 + [i, i] + [vp] * 3 + [sz, vp, vp]
+        L.ssm_delta_bwd.restype = i
+        L.ssm_delta_bwd.argtypes = [i] * 7 + [u, vp] + [vp] * 7 + [i, i] + [vp] * 9 + [sz, vp, vp]
+        L.ssm_delta_update.restype = i
+        L.ssm_delta_update.argtypes = [i] * 6 + [vp, vp, i] + [vp] * 6 + [i, vp, vp, vp]
+        L.ssm_group_norm_fwd.restype = i
+        L.ssm_group_norm_fwd.argtypes = [i] * 5 + [u, vp] + [vp] * 4 + [i, vp, vp, vp]
+        L.ssm_group_norm_bwd_workspace_bytes.restype = sz
+        L.ssm_group_norm_bwd_workspace_bytes.argtypes = [i] * 4
+        L.ssm_group_norm_bwd.restype = i
+        L.ssm_group_norm_bwd.argtypes = [i] * 5 + [u, vp] + [vp] * 4 + [i] + [vp] * 6 + [sz, vp, vp]
         _lib = L
     return _lib
 
@@ -747,6 +795,238 @@ def ssm_conv1d_update(state, x, weight, *, bias=None, silu=True, out_dtype=None,
     return y
 
 
+def _layout(cls, ts, names, shapes, dtypes):
+    """Pointers and the layout struct `cls` of tensors whose last index (for a
+    shape of 4, or of 3 where `cls` has no head stride) is contiguous.  The
+    dimensions before it are batch, step and (where `cls` has it) head; 0
+    stands for the stride of a dimension of size 1 and of an absent tensor."""
+    fields = [n for n, _ in cls._fields_]
+    order = [n for n in ("batch", "step", "head") if n in fields]
+    out, ptrs = cls(), []
+    for j, (t, name, shape, dtype) in enumerate(zip(ts, names, shapes, dtypes)):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+        if t.shape != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        _no_broadcast(t, name)
+        if len(shape) > len(order) and shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError("%s must have a contiguous last index" % name)
+        for d, n in enumerate(order):
+            getattr(out, n)[j] = t.stride(d) if shape[d] > 1 else 0
+        ptrs.append(t.data_ptr())
+    for t, name in zip(ts, names):
+        if t is not None and not t.is_cuda:
+            raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    return ptrs, out
+
+
+def _float(v):
+    return None if v is None else ctypes.byref(ctypes.c_float(v))
+
+
+def _delta_sizes(q, v, cu_seqlens):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [batch, L, qk_heads, K] and v [batch, L, heads, V]")
+    batch, L, hk, K = q.shape
+    nseq = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 2:
+            raise TypeError("cu_seqlens must be an int32 tensor of (sequences + 1) entries")
+        nseq = cu_seqlens.numel() - 1
+    return batch, L, hk, K, v.shape[2], v.shape[3], nseq
+
+
+def ssm_delta_bwd_workspace(q, v, *, cu_seqlens=None):
+    """A device buffer of ssm_delta_bwd_workspace_bytes(...) bytes for these
+    inputs: `checkpoints` of ssm_delta_fwd and `workspace` of ssm_delta_bwd."""
+    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
+    need = lib().ssm_delta_bwd_workspace_bytes(batch, L, hk, H, K, V, nseq)
+    return torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
+
+
+@_on_caller_stream
+def ssm_delta_fwd(q, k, v, g, beta, *, scale=None, h0=None, cu_seqlens=None, out_dtype=None,
+                  return_final_state=True, y=None, hL=None, checkpoints=None, workspace=None,
+                  stream=None):
+    """The gated delta rule over whole sequences; returns (y, hL).
+    q, k [batch, L, qk_heads, K], v and y [batch, L, heads, V], g (log decay)
+    and beta [batch, L, heads] fp32, in any order of the first three strides
+    (slices of one projection's output, [batch, heads, L, .] tensors
+    transposed); h0, hL [sequences, heads, K, V] fp32.  scale defaults to
+    K ** -0.5, out_dtype to v's dtype.
+    cu_seqlens: int32 device tensor of sequence bounds for sequences packed
+    into one batch row.  checkpoints: a buffer from ssm_delta_bwd_workspace
+    that receives what ssm_delta_bwd reads (checkpoints_in_workspace=True)."""
+    _no_broadcast_args(q=q, k=k, v=v, g=g, beta=beta, h0=h0, y=y, hL=hL)
+    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
+    ind, f32, dev = v.dtype, torch.float32, v.device
+    out_dtype = y.dtype if y is not None else (out_dtype or ind)
+    state = (nseq or batch, H, K, V)
+    if y is None:
+        y = torch.empty((batch, L, H, V), dtype=out_dtype, device=dev)
+    if hL is None and return_final_state:
+        hL = torch.empty(state, dtype=f32, device=dev)
+    (qp, kp, vp, yp, gp, bp), layout = _layout(
+        DeltaLayout, (q, k, v, y, g, beta), ("q", "k", "v", "y", "g", "beta"),
+        ((batch, L, hk, K), (batch, L, hk, K), (batch, L, H, V), (batch, L, H, V), (batch, L, H), (batch, L, H)),
+        (ind, ind, ind, out_dtype, f32, f32))
+    flags, ws = 0, workspace
+    if checkpoints is not None:
+        flags, ws = SSM_FLAG_CHECKPOINTS, checkpoints
+    elif ws is None:
+        need = lib().ssm_delta_fwd_workspace_bytes(batch, L, hk, H, K, V, nseq)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = lib().ssm_delta_fwd(
+        batch, L, hk, H, K, V, _dtype_code(ind), flags, _float(scale), qp, kp, vp,
+        gp, bp, _ptr(h0, "h0", state, f32), _ptr(cu_seqlens, "cu_seqlens"), nseq, _dtype_code(out_dtype), yp,
+        _ptr(hL, "hL", state, f32), _ptr(ws, "workspace"),
+        0 if ws is None else ws.numel() * ws.element_size(), ctypes.byref(layout), _stream(stream, dev))
+    _check(st)
+    return y, hL
+
+
+@_on_caller_stream
+def ssm_delta_bwd(q, k, v, g, beta, dy, *, scale=None, h0=None, dhL=None, cu_seqlens=None,
+                  workspace=None, checkpoints_in_workspace=False, dq=None, dk=None, dv=None,
+                  stream=None):
+    """Gradients of ssm_delta_fwd; returns a dict with dq, dk, dv (dy's dtype),
+    dg, dbeta and dh0 (fp32).  workspace: from ssm_delta_bwd_workspace
+    (allocated here when not given); checkpoints_in_workspace=True when
+    ssm_delta_fwd filled it for the same inputs."""
+    _no_broadcast_args(q=q, k=k, v=v, g=g, beta=beta, dy=dy, h0=h0, dhL=dhL, dq=dq, dk=dk, dv=dv)
+    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
+    ind, gt, f32, dev = v.dtype, dy.dtype, torch.float32, v.device
+    state = (nseq or batch, H, K, V)
+    if workspace is None:
+        if checkpoints_in_workspace:
+            raise ValueError("checkpoints_in_workspace needs the workspace that ssm_delta_fwd filled")
+        workspace = ssm_delta_bwd_workspace(q, v, cu_seqlens=cu_seqlens)
+    new = lambda t, *shape: torch.empty(shape, dtype=gt, device=dev) if t is None else t  # noqa: E731
+    out = {"dq": new(dq, batch, L, hk, K), "dk": new(dk, batch, L, hk, K), "dv": new(dv, batch, L, H, V),
+           "dg": torch.empty((batch, L, H), dtype=f32, device=dev),
+           "dbeta": torch.empty((batch, L, H), dtype=f32, device=dev),
+           "dh0": torch.empty(state, dtype=f32, device=dev)}
+    qk, vy, gate = (batch, L, hk, K), (batch, L, H, V), (batch, L, H)
+    (qp, kp, vp, gp, bp, dyp, dqp, dkp, dvp), layout = _layout(
+        DeltaBwdLayout, (q, k, v, g, beta, dy, out["dq"], out["dk"], out["dv"]),
+        ("q", "k", "v", "g", "beta", "dy", "dq", "dk", "dv"), (qk, qk, vy, gate, gate, vy, qk, qk, vy),
+        (ind, ind, ind, f32, f32, gt, gt, gt, gt))
+    st = lib().ssm_delta_bwd(
+        batch, L, hk, H, K, V, _dtype_code(ind), SSM_FLAG_CHECKPOINTS if checkpoints_in_workspace else 0,
+        _float(scale), qp, kp, vp, gp, bp, _ptr(h0, "h0", state, f32),
+        _ptr(cu_seqlens, "cu_seqlens"), nseq, _dtype_code(gt), dyp, _ptr(dhL, "dhL", state, f32), dqp, dkp, dvp,
+        _ptr(out["dg"], "dg"), _ptr(out["dbeta"], "dbeta"), _ptr(out["dh0"], "dh0"), _ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), ctypes.byref(layout), _stream(stream, dev))
+    _check(st)
+    return out
+
+
+@_on_caller_stream
+def ssm_delta_update(state, q, k, v, g, beta, *, scale=None, slots=None, out_dtype=None, y=None,
+                     stream=None):
+    """One decode step of the gated delta rule; updates `state` [slots, heads,
+    K, V] (fp32) in place and returns y [batch, heads, V].  q, k [batch,
+    qk_heads, K], v [batch, heads, V], g and beta [batch, heads].  slots:
+    int32 device tensor with each row's state (None: row b uses state b; a
+    negative or too large slot skips the row, its y is zero)."""
+    _no_broadcast_args(state=state, q=q, k=k, v=v, g=g, beta=beta, y=y)
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [batch, qk_heads, K], v [batch, heads, V], state [slots, heads, K, V]")
+    batch, hk, K = q.shape
+    H, V = v.shape[1:]
+    ind, f32 = v.dtype, torch.float32
+    out_dtype = y.dtype if y is not None else (out_dtype or ind)
+    if y is None:
+        y = torch.empty((batch, H, V), dtype=out_dtype, device=v.device)
+    if slots is None and state.shape[0] != batch:
+        raise ValueError("state has %d entries for %d rows (pass slots)" % (state.shape[0], batch))
+    with_step = lambda t: None if t is None else t.unsqueeze(1)  # noqa: E731
+    qk, vy, gate = (batch, 1, hk, K), (batch, 1, H, V), (batch, 1, H)
+    (qp, kp, vp, yp, gp, bp), layout = _layout(
+        DeltaLayout, [with_step(t) for t in (q, k, v, y, g, beta)], ("q", "k", "v", "y", "g", "beta"),
+        (qk, qk, vy, vy, gate, gate), (ind, ind, ind, out_dtype, f32, f32))
+    st = lib().ssm_delta_update(
+        batch, hk, H, K, V, _dtype_code(ind), _float(scale),
+        _ptr(state, "state", (state.shape[0], H, K, V), f32), state.shape[0],
+        _ptr(slots, "slots", (batch,), torch.int32), qp, kp, vp, gp, bp, _dtype_code(out_dtype), yp,
+        ctypes.byref(layout), _stream(stream, v.device))
+    _check(st)
+    return y
+
+
+def _norm_flags(rms, silu, gate_first):
+    return ((SSM_NORM_RMS if rms else 0) | (SSM_NORM_SILU if silu else 0)
+            | (SSM_NORM_GATE_FIRST if gate_first else 0))
+
+
+def _norm_3d(t):
+    return t.unsqueeze(1) if isinstance(t, torch.Tensor) and t.dim() == 2 else t
+
+
+@_on_caller_stream
+def ssm_group_norm_fwd(x, groups, *, weight=None, bias=None, z=None, eps=1e-5, rms=False, silu=False,
+                       gate_first=False, out_dtype=None, y=None, stream=None):
+    """Norm over groups of channels of one step, with an activation; returns y.
+    x, z, y: [batch, L, dim] or [batch, dim] (channels contiguous, step and
+    batch strides free); weight, bias [dim] fp32.  a = normalise(x) * weight +
+    bias; y = a, silu(a) (silu=True) or a * silu(z) (z given); with gate_first
+    x * silu(z) is normalised and y = a.  rms: no mean is subtracted.
+    out_dtype defaults to x's dtype."""
+    _no_broadcast_args(x=x, weight=weight, bias=bias, z=z, y=y)
+    out_dtype = y.dtype if y is not None else (out_dtype or x.dtype)
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+    x3, z3, y3 = _norm_3d(x), _norm_3d(z), _norm_3d(y)
+    if x3.dim() != 3:
+        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
+    batch, L, dim = x3.shape
+    (xp, zp, yp), layout = _layout(NormLayout, (x3, z3, y3), ("x", "z", "y"), (x3.shape,) * 3,
+                                   (x.dtype, x.dtype, out_dtype))
+    st = lib().ssm_group_norm_fwd(
+        batch, L, dim, groups, _dtype_code(x.dtype), _norm_flags(rms, silu, gate_first), _float(eps), xp,
+        _ptr(weight, "weight", (dim,), torch.float32), _ptr(bias, "bias", (dim,), torch.float32), zp,
+        _dtype_code(out_dtype), yp, ctypes.byref(layout), _stream(stream, x.device))
+    _check(st)
+    return y
+
+
+@_on_caller_stream
+def ssm_group_norm_bwd(x, groups, dy, *, weight=None, bias=None, z=None, eps=1e-5, rms=False, silu=False,
+                       gate_first=False, dx=None, dz=None, workspace=None, stream=None):
+    """Gradients of ssm_group_norm_fwd; returns a dict with dx, dz (None without
+    z), dweight and dbias (None where weight or bias is not given).  dx and dz
+    have dy's dtype, dweight and dbias are fp32."""
+    _no_broadcast_args(x=x, weight=weight, bias=bias, z=z, dy=dy, dx=dx, dz=dz)
+    gt, dev, f32 = dy.dtype, x.device, torch.float32
+    dx = torch.empty(x.shape, dtype=gt, device=dev) if dx is None else dx
+    if z is not None and dz is None:
+        dz = torch.empty(x.shape, dtype=gt, device=dev)
+    ts = [_norm_3d(t) for t in (x, z, dy, dx, dz)]
+    if ts[0].dim() != 3:
+        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
+    batch, L, dim = ts[0].shape
+    dw = torch.empty(dim, dtype=f32, device=dev) if weight is not None else None
+    db = torch.empty(dim, dtype=f32, device=dev) if bias is not None else None
+    if workspace is None and (dw is not None or db is not None):
+        need = lib().ssm_group_norm_bwd_workspace_bytes(batch, L, dim, groups)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+    (xp, zp, dyp, dxp, dzp), layout = _layout(NormBwdLayout, ts, ("x", "z", "dy", "dx", "dz"),
+                                              (ts[0].shape,) * 5, (x.dtype, x.dtype, gt, gt, gt))
+    st = lib().ssm_group_norm_bwd(
+        batch, L, dim, groups, _dtype_code(x.dtype), _norm_flags(rms, silu, gate_first), _float(eps), xp,
+        _ptr(weight, "weight", (dim,), f32), _ptr(bias, "bias", (dim,), f32), zp, _dtype_code(gt), dyp, dxp, dzp,
+        _ptr(dw, "dweight"), _ptr(db, "dbias"), _ptr(workspace, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), ctypes.byref(layout),
+        _stream(stream, dev))
+    _check(st)
+    return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
+
+
 scan_fwd = ssm_scan_fwd
 scan_bwd = ssm_scan_bwd
 scan_bwd_bld = ssm_scan_bwd_bld
@@ -754,3 +1034,8 @@ state_update = ssm_state_update
 conv1d_fwd = ssm_conv1d_fwd
 conv1d_fwd_bld = ssm_conv1d_fwd_bld
 conv1d_update = ssm_conv1d_update
+delta_fwd = ssm_delta_fwd
+delta_bwd = ssm_delta_bwd
+delta_update = ssm_delta_update
+group_norm_fwd = ssm_group_norm_fwd
+group_norm_bwd = ssm_group_norm_bwd

@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libssm.so")
 PEAKS_LIB = os.path.join(HERE, "libssm_peaks.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["ssm_api.hip", "scan_fwd.hip", "scan_bld.hip", "state_update.hip", "conv1d.hip",
-           "scan_bwd.hip", "transpose.hip"]
+           "scan_bwd.hip", "transpose.hip", "delta_api.hip", "delta_step.hip", "delta_fwd.hip",
+           "delta_bwd.hip", "group_norm.hip"]
 ARCH = "gfx950"
 # Packed fp32 VALU ops are kept out of the generated code on purpose.
 HIPFLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

@@ -1,0 +1,726 @@
+// delta_bwd.hip -- gradients of the gated delta rule (gfx950; C ABI in
+// include/ssm_delta.h).
+//
+// In the chunk form of delta_fwd.hip, with dS1 the gradient of the state
+// leaving the chunk (tail = e^{Gc - G}):
+//     dU = P^T dY + tail (K dS1),   dX = T^T dU,   dV = beta dX
+//     dS0 = e^{Gc} dS1 + Q^T (scale e^G dY) - K^T (beta e^G dX)
+// is a recurrence over the chunks from last to first whose columns are
+// independent, as the forward's: delta_scan_bwd_kernel runs it with the state's
+// gradient in registers and leaves dS1 and dX of every chunk in the
+// workspace, beside the forward's S0 and U.  What sums over the value
+// channels is then done for all chunks at once (delta_grad_kernel):
+//     dP = scale Gam (dY U^T) (i >= j),   dM = -Gam (dX U^T) (i > j),
+//     dQ = scale e^G (dY S0^T) + dP K
+//     dK = tail (U dS1^T) - beta e^G (dX S0^T) + dP^T Q + (N + N^T) K,
+//          N = beta dM
+//     dbeta = dX . V - e^G k . (dX S0^T) + rowsum(dM (K K^T))
+// with Gam_ij = e^{G_i - G_j}.  A log decay g_m stands in every exponential
+// that spans step m, so its gradient is the sum over those terms only (no
+// difference of running sums):
+//     dg_m = sum_{i >= m > j} W_ij + sum_{i >= m} (scale e^{G_i} q_i.(dY S0^T)_i
+//            - beta_i e^{G_i} k_i.(dX S0^T)_i) + sum_{j < m} tail_j k_j.(U dS1^T)_j
+//            + e^{Gc} <S0, dS1>,      W = dP (Q K^T) + N (K K^T)
+#include "delta_chunk.hpp"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// bf16 terms of dY
+template <typename T, typename TG, int KD>
+constexpr int kGradTerms = sizeof(TG) == 2 ? 1 : Terms<T, KD>::kSum;
+
+template <typename TG> __device__ inline void store_grad(TG *p, float v)
+{
+    if constexpr (sizeof(TG) == 2) p->bits = uint16_t(pack_bf16x2(v, v));
+    else *p = v;
+}
+
+// ------------------------------------------------------------ the recurrence
+struct ScanBwdParams {
+    int seqlen, rep, h, K, V, Vp;
+    int vec_q, vec_k;
+    float scale;
+    const int *cu;
+    const void *q, *k, *dy;
+    const float *dhL;
+    void *dv;
+    float *dh0;
+    DeltaStride sq, sk, sdy, sdv;
+    DeltaWs ws;
+};
+
+template <typename T, typename TG, int KD>
+__global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdParams p)
+{
+    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NG = kGradTerms<T, TG, KD>;
+    constexpr int NCH = KD / 8, kTile = 64 * KD, KB = KD / 32;
+    constexpr int kTri = kTriFrags * NS * 512, kTriLoads = (kTri / 8 + kThreads - 1) / kThreads;
+    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile], tt[kTri], pt[kTri];
+    __shared__ __align__(16) float vec[256];
+
+    const int head = int(blockIdx.y), tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63;
+    const int r = l & 15, g = l >> 4;
+    const int col = int(blockIdx.x) * 64 + 16 * wave + r;
+    const bool mine = col < p.V;
+    const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
+    const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
+    const long long state_at = ((long long)blockIdx.z * p.h + head) * p.K * (long long)p.V + col;
+
+    const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h;
+    const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h;
+    const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + seq.first * p.sdy.t + head * p.sdy.h + col;
+    TG *vp = static_cast<TG *>(p.dv) + seq.batch * p.sdv.b + seq.first * p.sdv.t + head * p.sdv.h + col;
+
+    // dS, laid out as S in the forward
+    f32x4 S[KD / 16];
+#pragma unroll
+    for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+            S[m][e] = p.dhL && mine && row < p.K ? p.dhL[state_at + (long long)row * p.V] : 0.0f;
+        }
+
+    TileLoad<T, NCH, kThreads> lk, lq;
+    u32x4 lt[kTriLoads], lp[kTriLoads];
+    float lv = 0.0f, dy[16];
+    auto fetch = [&](int c) {
+        const int rows = seq.len - c * kDeltaChunk;
+        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
+        lk.fetch(kp + t * p.sk.t, p.sk.t, rows, p.K, p.vec_k);
+        lq.fetch(qp + t * p.sq.t, p.sq.t, rows, p.K, p.vec_q);
+        const u32x4 *T0 = reinterpret_cast<const u32x4 *>(p.ws.Tt + rec * kTri);
+        const u32x4 *P0 = reinterpret_cast<const u32x4 *>(p.ws.Pt + rec * kTri);
+#pragma unroll
+        for (int i = 0; i < kTriLoads; ++i) {
+            const int at = tid + i * kThreads;
+            if (at < kTri / 8) {
+                lt[i] = T0[at];
+                lp[i] = P0[at];
+            }
+        }
+        lv = p.ws.vec[rec * 256 + tid];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * m + 4 * g + e;
+                dy[4 * m + e] = mine && i < rows ? io<TG>::load1(yp + (t + i) * p.sdy.t) : 0.0f;
+            }
+    };
+    if (chunks > 0) fetch(chunks - 1);
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int rows = seq.len - c * kDeltaChunk;
+        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
+        __syncthreads();  // the last chunk's reads are done
+        lk.template store<NI>(kt);
+        lq.template store<NI>(qt);
+#pragma unroll
+        for (int i = 0; i < kTriLoads; ++i) {
+            const int at = tid + i * kThreads;
+            if (at < kTri / 8) {
+                reinterpret_cast<u32x4 *>(tt)[at] = lt[i];
+                reinterpret_cast<u32x4 *>(pt)[at] = lp[i];
+            }
+        }
+        vec[tid] = lv;
+        f32x4 Y[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) Y[m] = f32x4{dy[4 * m], dy[4 * m + 1], dy[4 * m + 2], dy[4 * m + 3]};
+        __syncthreads();
+        if (c > 0) fetch(c - 1);
+
+        {
+            float *s = p.ws.dS1 + rec * KD * p.Vp + col;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+        }
+        // dU = P^T dY + tail (K dS)
+        f32x4 U[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) U[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                Frag<NI> a;
+#pragma unroll
+                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
+                U[m] = mma<NI, NS>(a, sb, U[m]);
+            }
+        }
+        {
+            const Frag<NG> yb[2] = {split8<NG>(Y[0], Y[1]), split8<NG>(Y[2], Y[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
+#pragma unroll
+                for (int b = m / 2; b < 2; ++b) {
+                    Frag<NS> a;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        a.t[n] = *reinterpret_cast<const bf16x8 *>(pt + ((tri_upper(m, b) * NS + n) * 64 + l) * 8);
+                    U[m] = mma<NS, NG>(a, yb[b], U[m]);
+                }
+            }
+        }
+        // dX = dU + (T - 1)^T dU
+        f32x4 X[4];
+        {
+            const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                X[m] = U[m];
+#pragma unroll
+                for (int b = m / 2; b < 2; ++b) {
+                    Frag<NS> a;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        a.t[n] = *reinterpret_cast<const bf16x8 *>(tt + ((tri_upper(m, b) * NS + n) * 64 + l) * 8);
+                    X[m] = mma<NS, NS>(a, ub[b], X[m]);
+                }
+            }
+        }
+        {
+            float *x = p.ws.dX + rec * 64 * p.Vp + col;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 bt = *reinterpret_cast<const f32x4 *>(vec + 192 + 16 * m + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * m + 4 * g + e;
+                    x[(long long)i * p.Vp] = X[m][e];
+                    if (mine && i < rows) store_grad(vp + (t + i) * p.sdv.t, bt[e] * X[m][e]);
+                }
+            }
+        }
+        // dS = e^{Gc} dS + Q^T (scale e^G dY) - K^T (beta e^G dX)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                Y[m][e] *= p.scale * eg[e];
+                X[m][e] *= -be[e];
+            }
+        }
+        {
+            const Frag<NS> yb[2] = {split8<NS>(Y[0], Y[1]), split8<NS>(Y[2], Y[3])};
+            const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
+            const float ec = vec[63];
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][e] *= ec;
+                const int col4 = 32 * (m / 2) + 8 * (r & 3) + 4 * (m % 2);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    Frag<NI> a;
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        a.t[n] = read_cols<NCH>(qt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
+                    S[m] = mma<NI, NS>(a, yb[b], S[m]);
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        a.t[n] = read_cols<NCH>(kt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
+                    S[m] = mma<NI, NS>(a, xb[b], S[m]);
+                }
+            }
+        }
+    }
+    if (p.dh0 && mine) {
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+                if (row < p.K) p.dh0[state_at + (long long)row * p.V] = S[m][e];
+            }
+    }
+}
+
+// ------------------------------------------------------------ sums over the value channels
+struct GradParams {
+    int seqlen, nseq, rep, h, K, V, Vp;
+    int vec_q, vec_k, vec_v, vec_dy;
+    float scale;
+    const int *cu;
+    const void *q, *k, *v, *dy;
+    const float *gate, *beta;
+    void *dq, *dk;
+    float *dg, *dbeta;
+    DeltaStride sq, sk, sv, sg, sbeta, sdy, sdq, sdk;
+    DeltaWs ws;
+};
+
+// Sum over 16 neighbouring lanes, to all of them.
+template <int kCtrl> __device__ inline float row_move(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, true));
+}
+__device__ inline float row_sum(float v)
+{
+    v += row_move<0xB1>(v);   // quad_perm 1,0,3,2
+    v += row_move<0x4E>(v);   // quad_perm 2,3,0,1
+    v += row_move<0x141>(v);  // row_half_mirror
+    v += row_move<0x140>(v);  // row_mirror
+    return v;
+}
+
+template <int N> __device__ inline float tile_value(const uint16_t *tile, int plane, int at)
+{
+    float v = 0.0f;
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) v += __uint_as_float(uint32_t(tile[n * plane + at]) << 16);
+    return v;
+}
+
+template <typename T, typename TG, int KD>
+__global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p)
+{
+    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NG = kGradTerms<T, TG, KD>;
+    constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;  // K and Q are staged KH columns at a time
+    constexpr int kHalves = KD / KH, NT = KH / 64, NTT = KD / 64;           // column tiles of a wave
+    constexpr int VB = sizeof(T) == 2 ? 64 : 32, NCV = VB / 8, kVTile = 64 * VB;
+    constexpr int kStage = (NG + 2 * NS) * kVTile * 2, kZ = 64 * 64, kZs = 2 * NS * kZ * 2, kW = 64 * 68 * 4;
+    constexpr int kUnion = kStage > kZs ? (kStage > kW ? kStage : kW) : (kZs > kW ? kZs : kW);
+    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile];
+    __shared__ __align__(16) unsigned char lds[kUnion];
+    __shared__ double G[64];
+    __shared__ __align__(16) float vec[256];
+    __shared__ float rowd[4][3][64], rect[4][64], row_v[64], row_m[64], dots[4];
+    uint16_t *ty = reinterpret_cast<uint16_t *>(lds), *tx = ty + NG * kVTile, *tu = tx + NS * kVTile;
+    uint16_t *zp = reinterpret_cast<uint16_t *>(lds), *zn = zp + NS * kZ;
+    float *W = reinterpret_cast<float *>(lds);
+
+    const int chunk = int(blockIdx.x), qk_head = int(blockIdx.y);
+    const int si = delta_seq_of(p.cu, p.nseq, p.seqlen, chunk);
+    const DeltaSeq seq = delta_seq(p.cu, si, p.seqlen);
+    const int at0 = (chunk - seq.chunk0) * kDeltaChunk;
+    const int rows = min(kDeltaChunk, seq.len - at0);
+    if (at0 < 0 || rows <= 0) return;  // the whole workgroup
+    const long long t0 = seq.first + at0;
+    const int tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63, r = l & 15, g = l >> 4;
+
+    const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + t0 * p.sk.t + qk_head * p.sk.h;
+    const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + t0 * p.sq.t + qk_head * p.sq.h;
+    auto stage_qk = [&](int half) {
+        TileLoad<T, NCH, kThreads> lk, lq;
+        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH, p.vec_k);
+        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH, p.vec_q);
+        lk.template store<NI>(kt);
+        lq.template store<NI>(qt);
+    };
+    if (kHalves == 1) stage_qk(0);
+
+    // column tile n of a wave: keys' entries key(n) + lane's r
+    auto key = [&](int n) { return (n / NT) * KH + wave * (KH / 4) + 16 * (n % NT); };
+    f32x4 dq[NTT][4], dk[NTT][4];
+#pragma unroll
+    for (int n = 0; n < NTT; ++n)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) dq[n][m] = dk[n][m] = f32x4{0, 0, 0, 0};
+
+    for (int hi = 0; hi < p.rep; ++hi) {
+        const int head = qk_head * p.rep + hi;
+        const long long rec = (long long)chunk * p.h + head;
+        __syncthreads();  // the last head's sums are read
+        vec[tid] = p.ws.vec[rec * 256 + tid];
+        if (wave == 0) {
+            float gi = 0.0f;
+            if (l < rows) gi = p.gate[seq.batch * p.sg.b + (t0 + l) * p.sg.t + head * p.sg.h];
+            G[l] = decay_sums(gi);
+        }
+        const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + t0 * p.sv.t + head * p.sv.h;
+        const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + t0 * p.sdy.t + head * p.sdy.h;
+        const float *U = p.ws.U + rec * 64 * p.Vp, *dX = p.ws.dX + rec * 64 * p.Vp;
+        const float *S0 = p.ws.S0 + rec * KD * p.Vp, *dS1 = p.ws.dS1 + rec * KD * p.Vp;
+
+        f32x4 ys[NTT][4], xs[NTT][4], us[NTT][4], dP[4], dM[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int n = 0; n < NTT; ++n) ys[n][m] = xs[n][m] = us[n][m] = f32x4{0, 0, 0, 0};
+            dP[m] = dM[m] = f32x4{0, 0, 0, 0};
+        }
+        constexpr int kPer = TileLoad<T, NCV, kThreads>::kPer;
+        float dot = 0.0f, xv[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) xv[i] = 0.0f;
+        for (int v0 = 0; v0 < p.V; v0 += VB) {
+            TileLoad<TG, NCV, kThreads> ly;
+            TileLoad<float, NCV, kThreads> lx, lu;
+            TileLoad<T, NCV, kThreads> lv;
+            ly.fetch(yp + v0, p.sdy.t, rows, p.V - v0, p.vec_dy);
+            lv.fetch(vp + v0, p.sv.t, rows, p.V - v0, p.vec_v);
+            lx.fetch(dX + v0, p.Vp, 64, VB, true);
+            lu.fetch(U + v0, p.Vp, 64, VB, true);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {  // dX . V of the thread's row
+                float x[8], v[8];
+                io<float>::unpack(lx.raw[i].w[0], x);
+                io<float>::unpack(lx.raw[i].w[1], x + 4);
+#pragma unroll
+                for (int w = 0; w < int(sizeof(T) / 2); ++w) io<T>::unpack(lv.raw[i].w[w], v + w * io<T>::kVec);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xv[i] = __builtin_fmaf(x[e], v[e], xv[i]);
+            }
+            __syncthreads();  // the last block's reads are done
+            ly.template store<NG>(ty);
+            lx.template store<NS>(tx);
+            lu.template store<NS>(tu);
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < VB / 32; ++b) {
+                Frag<NG> ay[4], yw;
+                Frag<NS> ax[4], au[4], xw;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+                        ay[m].t[n] = read_row<NCV>(ty + n * kVTile, 16 * m + r, 4 * b + g);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        ax[m].t[n] = read_row<NCV>(tx + n * kVTile, 16 * m + r, 4 * b + g);
+                        au[m].t[n] = read_row<NCV>(tu + n * kVTile, 16 * m + r, 4 * b + g);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NG; ++n) yw.t[n] = read_row<NCV>(ty + n * kVTile, 16 * wave + r, 4 * b + g);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) xw.t[n] = read_row<NCV>(tx + n * kVTile, 16 * wave + r, 4 * b + g);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c <= wave) {  // row tile `wave` of dY U^T and dX U^T
+                        dP[c] = mma<NG, NS>(yw, au[c], dP[c]);
+                        dM[c] = mma<NS, NS>(xw, au[c], dM[c]);
+                    }
+#pragma unroll
+                for (int n = 0; n < NTT; ++n) {
+                    const long long at = (long long)(key(n) + r) * p.Vp + v0 + 32 * b + 8 * g;
+                    const f32x4 s0 = *reinterpret_cast<const f32x4 *>(S0 + at);
+                    const f32x4 s1 = *reinterpret_cast<const f32x4 *>(S0 + at + 4);
+                    const f32x4 d0 = *reinterpret_cast<const f32x4 *>(dS1 + at);
+                    const f32x4 d1 = *reinterpret_cast<const f32x4 *>(dS1 + at + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dot = __builtin_fmaf(s0[e], d0[e], __builtin_fmaf(s1[e], d1[e], dot));
+                    const Frag<NS> sb = split8<NS>(s0, s1), db = split8<NS>(d0, d1);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        ys[n][m] = mma<NG, NS>(ay[m], sb, ys[n][m]);
+                        xs[n][m] = mma<NS, NS>(ax[m], sb, xs[n][m]);
+                        us[n][m] = mma<NS, NS>(au[m], db, us[n][m]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            float s = xv[i];
+#pragma unroll
+            for (int o = 1; o < NCV; o *= 2) s += __shfl_xor(s, o);
+            if (tid % NCV == 0) row_v[(tid + i * kThreads) / NCV] = s;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
+        if (l == 0) dots[wave] = dot;
+
+        // Q K^T, K K^T again, and the row sums that dg and dbeta need
+        f32x4 kk[4], qk[4], rq[4], rr[4], ru[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) kk[m] = qk[m] = rq[m] = rr[m] = ru[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+            if (kHalves > 1) {
+                __syncthreads();
+                stage_qk(half);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < KH / 32; ++b) {
+                Frag<NI> ka, qa;
+#pragma unroll
+                for (int n = 0; n < NI; ++n) {
+                    ka.t[n] = read_row<NCH>(kt + n * kTile, 16 * wave + r, 4 * b + g);
+                    qa.t[n] = read_row<NCH>(qt + n * kTile, 16 * wave + r, 4 * b + g);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c <= wave) {
+                        Frag<NI> kb;
+#pragma unroll
+                        for (int n = 0; n < NI; ++n)
+                            kb.t[n] = read_row<NCH>(kt + n * kTile, 16 * c + r, 4 * b + g);
+                        kk[c] = mma<NI, NI>(ka, kb, kk[c]);
+                        qk[c] = mma<NI, NI>(qa, kb, qk[c]);
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int c = wave * (KH / 4) + 16 * n + r;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = chunk_at<NCH>(16 * m + 4 * g + e, c >> 3) + (c & 7);
+                        const float kv = tile_value<NI>(kt, kTile, at), qv = tile_value<NI>(qt, kTile, at);
+                        rq[m][e] = __builtin_fmaf(qv, ys[half * NT + n][m][e], rq[m][e]);
+                        rr[m][e] = __builtin_fmaf(kv, xs[half * NT + n][m][e], rr[m][e]);
+                        ru[m][e] = __builtin_fmaf(kv, us[half * NT + n][m][e], ru[m][e]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = row_sum(rq[m][e]), b = row_sum(rr[m][e]), c = row_sum(ru[m][e]);
+                if (r == 0) {
+                    const int i = 16 * m + 4 * g + e;
+                    rowd[wave][0][i] = a;
+                    rowd[wave][1][i] = b;
+                    rowd[wave][2][i] = c;
+                }
+            }
+        // dP, N = beta dM, W (the staged tiles are read: W takes their place)
+        f32x4 sums = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int j = 16 * c + r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * wave + 4 * g + e;
+                float w = 0.0f;
+                if (c <= wave) {
+                    const float d = i >= j ? exp2_hw(float(G[i] - G[j]) * kLog2e) : 0.0f;
+                    dP[c][e] *= p.scale * d;
+                    const float mm = i > j ? -d * dM[c][e] : 0.0f;
+                    sums[e] = __builtin_fmaf(mm, kk[c][e], sums[e]);
+                    dM[c][e] = vec[192 + i] * mm;
+                    if (i > j) w = dP[c][e] * qk[c][e] + dM[c][e] * kk[c][e];
+                }
+                W[i * 68 + j] = w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float s = row_sum(sums[e]);
+            if (r == 0) row_m[16 * wave + 4 * g + e] = s;
+        }
+        __syncthreads();
+        {   // W_ij <- sum of W_i before j: four threads a row
+            float *w = W + (tid >> 2) * 68 + (tid & 3) * 16;
+            f32x4 x[4];
+            float run = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = reinterpret_cast<f32x4 *>(w)[i];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float v = x[i / 4][i % 4];
+                x[i / 4][i % 4] = run;
+                run += v;
+            }
+            const float a = __shfl_up(run, 1), b = __shfl_up(run, 2), c = __shfl_up(run, 3);
+            const int quarter = tid & 3;
+            const float before = (quarter > 0 ? a : 0.0f) + (quarter > 1 ? b : 0.0f) + (quarter > 2 ? c : 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][e] += before;
+                reinterpret_cast<f32x4 *>(w)[i] = x[i];
+            }
+        }
+        __syncthreads();
+        {   // sum over i >= m of those, a quarter of the rows a wave
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (16 * wave + i >= l) s += W[(16 * wave + i) * 68 + l];
+            rect[wave][l] = s;
+        }
+        __syncthreads();
+        if (wave == 0) {
+            const float eg = vec[l], tail = vec[64 + l], be = vec[128 + l];
+            float a[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) a[i] = rowd[0][i][l] + rowd[1][i][l] + rowd[2][i][l] + rowd[3][i][l];
+            const float here = p.scale * eg * a[0] - be * a[1], wr = tail * a[2];
+            float after = here, before = wr;  // sums over i >= l and over j <= l
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) {
+                const float x = __shfl_down(after, o), y = __shfl_up(before, o);
+                if (l + o < 64) after += x;
+                if (l >= o) before += y;
+            }
+            before = __shfl_up(before, 1);
+            if (l == 0) before = 0.0f;
+            const float inner = rect[0][l] + rect[1][l] + rect[2][l] + rect[3][l];
+            const float state = vec[63] * (dots[0] + dots[1] + dots[2] + dots[3]);
+            if (l < rows) {
+                const long long at = ((long long)seq.batch * p.seqlen + t0 + l) * p.h + head;
+                p.dg[at] = inner + after + before + state;
+                p.dbeta[at] = row_v[l] - eg * a[1] + row_m[l];
+            }
+        }
+        // dP and N transposed into LDS: row j, columns i
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c <= wave || (c == wave + 1 && wave % 2 == 0)) {
+                const int at = chunk_at<8>(16 * c + r, 2 * wave + (g >> 1)) + 4 * (g & 1);
+                float a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    a[e] = c <= wave ? dP[c][e] : 0.0f;
+                    b[e] = c <= wave ? dM[c][e] : 0.0f;
+                }
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+                    const u32x2 x = {split_pair(a[0], a[1]), split_pair(a[2], a[3])};
+                    const u32x2 y = {split_pair(b[0], b[1]), split_pair(b[2], b[3])};
+                    *reinterpret_cast<u32x2 *>(zp + n * kZ + at) = x;
+                    *reinterpret_cast<u32x2 *>(zn + n * kZ + at) = y;
+                }
+            }
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+            if (kHalves > 1) {
+                __syncthreads();
+                stage_qk(half);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                Frag<NI> kb[NT], qb[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int col4 = wave * (KH / 4) + 16 * n + 4 * (r & 3);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        kb[n].t[i] = read_cols<NCH>(kt + i * kTile, 32 * b + 8 * g, 32 * b + 8 * g + 4, col4);
+                        qb[n].t[i] = read_cols<NCH>(qt + i * kTile, 32 * b + 8 * g, 32 * b + 8 * g + 4, col4);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    Frag<NS> a, z;
+                    if (b <= m / 2) {  // rows i: dP K and N K
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) {
+                            a.t[i] = read_cols<8>(zp + i * kZ, 32 * b + 8 * g, 32 * b + 8 * g + 4, 16 * m + 4 * (r & 3));
+                            z.t[i] = read_cols<8>(zn + i * kZ, 32 * b + 8 * g, 32 * b + 8 * g + 4, 16 * m + 4 * (r & 3));
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            dq[half * NT + n][m] = mma<NS, NI>(a, kb[n], dq[half * NT + n][m]);
+                            dk[half * NT + n][m] = mma<NS, NI>(z, kb[n], dk[half * NT + n][m]);
+                        }
+                    }
+                    if (b >= m / 2) {  // rows j: dP^T Q and N^T K
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) {
+                            a.t[i] = read_row<8>(zp + i * kZ, 16 * m + r, 4 * b + g);
+                            z.t[i] = read_row<8>(zn + i * kZ, 16 * m + r, 4 * b + g);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            dk[half * NT + n][m] = mma<NS, NI>(a, qb[n], dk[half * NT + n][m]);
+                            dk[half * NT + n][m] = mma<NS, NI>(z, kb[n], dk[half * NT + n][m]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
+            const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
+#pragma unroll
+            for (int n = 0; n < NTT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dq[n][m][e] = __builtin_fmaf(p.scale * eg[e], ys[n][m][e], dq[n][m][e]);
+                    dk[n][m][e] += tail[e] * us[n][m][e] - be[e] * xs[n][m][e];
+                }
+        }
+    }
+    TG *dqp = static_cast<TG *>(p.dq) + seq.batch * p.sdq.b + t0 * p.sdq.t + qk_head * p.sdq.h;
+    TG *dkp = static_cast<TG *>(p.dk) + seq.batch * p.sdk.b + t0 * p.sdk.t + qk_head * p.sdk.h;
+#pragma unroll
+    for (int n = 0; n < NTT; ++n) {
+        const int c = key(n) + r;
+        if (c >= p.K) continue;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * m + 4 * g + e;
+                if (i < rows) {
+                    store_grad(dqp + i * p.sdq.t + c, dq[n][m][e]);
+                    store_grad(dkp + i * p.sdk.t + c, dk[n][m][e]);
+                }
+            }
+    }
+}
+
+template <typename T, typename TG, int KD>
+hipError_t launch_typed(const DeltaBwdArgs &b, const DeltaWs &ws, hipStream_t stream)
+{
+    const DeltaArgs &a = b.f;
+    const int es = sizeof(T), gs = sizeof(TG), rep = a.h / a.hk, Vp = delta_vp(a.V);
+    const int vq = delta_vec(a.q, a.sq, a.K, es, a, a.hk), vk = delta_vec(a.k, a.sk, a.K, es, a, a.hk);
+    const ScanBwdParams sp{a.seqlen, rep, a.h, a.K, a.V, Vp, vq, vk, a.scale, a.cu, a.q, a.k, b.dy, b.dhL, b.dv,
+                           b.dh0, a.sq, a.sk, b.sdy, b.sdv, ws};
+    const GradParams gp{a.seqlen, a.nseq, rep, a.h, a.K, a.V, Vp, vq, vk, delta_vec(a.v, a.sv, a.V, es, a, a.h),
+                        delta_vec(b.dy, b.sdy, a.V, gs, a, a.h), a.scale, a.cu, a.q, a.k, a.v, b.dy, a.g, a.beta,
+                        b.dq, b.dk, b.dg, b.dbeta, a.sq, a.sk, a.sv, a.sg, a.sbeta, b.sdy, b.sdq, b.sdk, ws};
+    const dim3 sgrid((a.V + 63) / 64, a.h, a.nseq);
+    const dim3 ggrid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.hk);
+    if (log_enabled())
+        log_line("delta_bwd: delta_scan_bwd_kernel, delta_grad_kernel<in %s, grad %s, K %d>, grids (%u, %u, %u), "
+                 "(%u, %u) x %d threads", type_tag<T>(), type_tag<TG>(), KD, sgrid.x, sgrid.y, sgrid.z, ggrid.x,
+                 ggrid.y, kThreads);
+    delta_scan_bwd_kernel<T, TG, KD><<<sgrid, dim3(kThreads), 0, stream>>>(sp);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    delta_grad_kernel<T, TG, KD><<<ggrid, dim3(kThreads), 0, stream>>>(gp);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t delta_bwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, int V, int num_seqs)
+{
+    size_t bytes = 0;
+    delta_ws(nullptr, delta_chunks(batch, seqlen, num_seqs) * h, K, V, true, &bytes);
+    return bytes;
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs &b, hipStream_t stream)
+{
+    const DeltaArgs &a = b.f;
+    const long long recs = delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0) * a.h;
+    const DeltaWs ws = delta_ws(a.workspace, recs, a.K, a.V, true, nullptr);
+    if (!b.ckpt_given) {  // the forward, for its records only
+        hipError_t e = launch_delta_prep(a, ws, true, stream);
+        if (e == hipSuccess) e = launch_delta_scan(a, ws, stream);
+        if (e != hipSuccess) return e;
+    }
+    return delta_dispatch(a.in_bf16, b.grad_bf16, a.K, [&](auto t, auto tg, auto kd) {
+        return launch_typed<decltype(t), decltype(tg), decltype(kd)::value>(b, ws, stream);
+    });
+}
+
+}  // namespace ssm

@@ -1,0 +1,493 @@
+// delta_fwd.hip -- the gated delta rule over whole sequences, a chunk of 64
+// steps at a time on the matrix cores (gfx950; C ABI in include/ssm_delta.h).
+//
+// With G_i the sum of the chunk's log decays up to step i, S0 the state
+// entering it, and U the rows beta_t (v_t - e^{g_t} S_{t-1}^T k_t):
+//     M_ij = beta_i e^{G_i - G_j} k_i . k_j  (i > j),    T = (1 + M)^-1
+//     P_ij = scale e^{G_i - G_j} q_i . k_j   (i >= j)
+//     X = beta (V - e^G K S0),   U = T X
+//     Y = scale e^G Q S0 + P U
+//     S1 = e^{Gc} S0 + K^T (e^{Gc - G} U)
+// M, T and P do not depend on the state: one workgroup per (chunk, head)
+// makes them (delta_prep_kernel) and leaves T - 1 and P in the workspace in
+// the order in which the matrix instruction reads them.  The columns of S
+// (the value channels) are independent of one another, so the recurrence
+// (delta_scan_kernel) gives each wave 16 columns of one head's state, kept in
+// registers over the whole sequence; every product's result is the next
+// one's right operand in place, and the four waves of a workgroup share only
+// the chunk's K, Q, T, P in LDS.
+#include "delta_chunk.hpp"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------ a chunk's matrices
+struct PrepParams {
+    int seqlen, nseq, rep, h, K;
+    int vec_q, vec_k;
+    float scale;
+    const int *cu;
+    const void *q, *k;
+    const float *g, *beta;
+    DeltaStride sq, sk, sg, sbeta;
+    DeltaWs ws;
+};
+
+constexpr int kPitch = 68;  // floats a row of the 64 x 64 matrices in LDS
+
+// (r, b) of fragment f
+__device__ inline void tri_place(bool upper, int f, int &r, int &b)
+{
+    if (upper) {
+        r = f < 4 ? f >> 1 : f - 2;
+        b = f < 4 ? f & 1 : 1;
+    } else {
+        r = f < 2 ? f : f >> 1;
+        b = f < 2 ? 0 : f & 1;
+    }
+    if (!upper && f >= 2) r = f < 4 ? 2 : 3;
+}
+
+// The fragments of a lower-triangular matrix m (or of its transpose); entries
+// with j + diag <= i are kept (diag 1: the strict part).
+template <int N, bool kUpper>
+__device__ inline void write_tri(const float *m, int diag, uint16_t *out)
+{
+    for (int it = int(threadIdx.x); it < kTriFrags * 64; it += kThreads) {
+        const int f = it >> 6, l = it & 63;
+        int r, b;
+        tri_place(kUpper, f, r, b);
+        const int row = 16 * r + (l & 15), g = l >> 4;
+        float v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const int col = 32 * b + 4 * g + (s & 3) + (s >= 4 ? 16 : 0);
+            const int i = kUpper ? col : row, j = kUpper ? row : col;
+            v[s] = j + diag <= i ? m[i * kPitch + j] : 0.0f;
+        }
+        const Frag<N> x = split8<N>(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            *reinterpret_cast<bf16x8 *>(out + ((f * N + n) * 64 + l) * 8) = x.t[n];
+    }
+}
+
+template <typename T, int KD, bool kBoth>
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p)
+{
+    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
+    constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;
+    constexpr int kTiles = 2 * NI * kTile * 2, kMats = 3 * 64 * kPitch * 4;
+    __shared__ __align__(16) unsigned char lds[kTiles > kMats ? kTiles : kMats];
+    __shared__ double G[64];
+    __shared__ float beta[64];
+    uint16_t *kt = reinterpret_cast<uint16_t *>(lds), *qt = kt + NI * kTile;
+    float *M = reinterpret_cast<float *>(lds), *P = M + 64 * kPitch, *Tm = P + 64 * kPitch;
+
+    const int chunk = int(blockIdx.x), head = int(blockIdx.y);
+    const int si = delta_seq_of(p.cu, p.nseq, p.seqlen, chunk);
+    const DeltaSeq sq = delta_seq(p.cu, si, p.seqlen);
+    const int at = (chunk - sq.chunk0) * kDeltaChunk;  // the chunk's first step in its sequence
+    const int rows = min(kDeltaChunk, sq.len - at);
+    if (at < 0 || rows <= 0) return;  // the whole workgroup: a record that no chunk uses
+    const long long rec = (long long)chunk * p.h + head, t0 = sq.first + at;
+    const int tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63, r = l & 15, g = l >> 4;
+
+    if (wave == 0) {
+        float gi = 0.0f, bi = 0.0f;
+        if (l < rows) {
+            gi = p.g[sq.batch * p.sg.b + (t0 + l) * p.sg.t + head * p.sg.h];
+            bi = p.beta[sq.batch * p.sbeta.b + (t0 + l) * p.sbeta.t + head * p.sbeta.h];
+        }
+        const double sum = decay_sums(gi);
+        G[l] = sum;
+        beta[l] = bi;
+        const double last = __shfl(sum, 63);
+        const float eg = exp2_hw(float(sum) * kLog2e);
+        float *vec = p.ws.vec + rec * 256;
+        vec[l] = eg;
+        vec[64 + l] = exp2_hw(float(last - sum) * kLog2e);
+        vec[128 + l] = bi * eg;
+        vec[192 + l] = bi;
+    }
+
+    // K K^T and Q K^T: wave w the tiles (w, 0..w)
+    const T *kp = static_cast<const T *>(p.k) + sq.batch * p.sk.b + t0 * p.sk.t + (head / p.rep) * p.sk.h;
+    const T *qp = static_cast<const T *>(p.q) + sq.batch * p.sq.b + t0 * p.sq.t + (head / p.rep) * p.sq.h;
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) kk[c] = qk[c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int half = 0; half < KD / KH; ++half) {
+        TileLoad<T, NCH, kThreads> lk, lq;
+        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH, p.vec_k);
+        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH, p.vec_q);
+        if (half) __syncthreads();
+        lk.template store<NI>(kt);
+        lq.template store<NI>(qt);
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < KH / 32; ++b) {
+            Frag<NI> ka, qa;
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                ka.t[n] = read_row<NCH>(kt + n * kTile, 16 * wave + r, 4 * b + g);
+                qa.t[n] = read_row<NCH>(qt + n * kTile, 16 * wave + r, 4 * b + g);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c <= wave) {
+                    Frag<NI> kb;
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        kb.t[n] = read_row<NCH>(kt + n * kTile, 16 * c + r, 4 * b + g);
+                    kk[c] = mma<NI, NI>(ka, kb, kk[c]);
+                    qk[c] = mma<NI, NI>(qa, kb, qk[c]);
+                }
+        }
+    }
+    __syncthreads();  // K, Q are read: M, P, T take their place
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c <= wave) {
+            const int j = 16 * c + r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * wave + 4 * g + e;
+                const float d = i >= j ? exp2_hw(float(G[i] - G[j]) * kLog2e) : 0.0f;
+                M[i * kPitch + j] = i > j ? beta[i] * d * kk[c][e] : 0.0f;
+                P[i * kPitch + j] = i >= j ? p.scale * d * qk[c][e] : 0.0f;
+            }
+        }
+    __syncthreads();
+
+    // T: the diagonal blocks by forward substitution, lane r one column (the
+    // four lane groups alike)
+    {
+        const float *m = M + (16 * wave) * kPitch + 16 * wave;
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == r ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v = __builtin_fmaf(-m[i * kPitch + j], t[j], v);
+            t[i] = v;
+        }
+        if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) Tm[(16 * wave + i) * kPitch + 16 * wave + r] = t[i];
+        }
+    }
+    __syncthreads();
+    // then the blocks below, T_ij = -T_ii sum_m M_im T_mj, in fp32 matrix
+    // instructions: distance d = i - j at a time, wave i its row
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+        if (wave >= d) {
+            const int j = wave - d;
+            f32x4 acc = {0, 0, 0, 0}, res = {0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < d; ++n) {
+                const int m = j + n;
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(M + (16 * wave + r) * kPitch + 16 * m + 4 * g);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    acc = mfma16_f32(a[s], Tm[(16 * m + 4 * g + s) * kPitch + 16 * j + r], acc);
+            }
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(Tm + (16 * wave + r) * kPitch + 16 * wave + 4 * g);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) res = mfma16_f32(a[s], acc[s], res);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Tm[(16 * wave + 4 * g + e) * kPitch + 16 * j + r] = -res[e];
+        }
+        __syncthreads();
+    }
+    constexpr long long kTri = kTriFrags * NS * 512;
+    write_tri<NS, false>(Tm, 1, p.ws.T + rec * kTri);
+    write_tri<NS, false>(P, 0, p.ws.P + rec * kTri);
+    if constexpr (kBoth) {
+        write_tri<NS, true>(Tm, 1, p.ws.Tt + rec * kTri);
+        write_tri<NS, true>(P, 0, p.ws.Pt + rec * kTri);
+    }
+}
+
+// ------------------------------------------------------------ the recurrence
+struct ScanParams {
+    int seqlen, rep, h, K, V, Vp;
+    int vec_q, vec_k, out_bf16;
+    float scale;
+    const int *cu;
+    const void *q, *k, *v;
+    const float *h0;
+    void *y;
+    float *hL;
+    DeltaStride sq, sk, sv, sy;
+    DeltaWs ws;
+};
+
+template <typename T, int KD>
+__global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p)
+{
+    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
+    constexpr int NCH = KD / 8, kTile = 64 * KD, KB = KD / 32;
+    constexpr int kTri = kTriFrags * NS * 512, kTriLoads = (kTri / 8 + kThreads - 1) / kThreads;
+    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile], tt[kTri], pt[kTri];
+    __shared__ __align__(16) float vec[256];
+
+    const int head = int(blockIdx.y), tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63;
+    const int r = l & 15, g = l >> 4;
+    const int col = int(blockIdx.x) * 64 + 16 * wave + r;
+    const bool mine = col < p.V;
+    const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
+    const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
+    const long long state_at = ((long long)blockIdx.z * p.h + head) * p.K * (long long)p.V + col;
+
+    const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h;
+    const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h;
+    const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + seq.first * p.sv.t + head * p.sv.h + col;
+    const long long y0 = seq.batch * p.sy.b + seq.first * p.sy.t + head * p.sy.h + col;
+
+    // S: tiles 2 b and 2 b + 1 hold the rows 32 b + 8 g + {0..3} and + {4..7}
+    f32x4 S[KD / 16];
+#pragma unroll
+    for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+            S[m][e] = p.h0 && mine && row < p.K ? p.h0[state_at + (long long)row * p.V] : 0.0f;
+        }
+
+    TileLoad<T, NCH, kThreads> lk, lq;
+    u32x4 lt[kTriLoads], lp[kTriLoads];
+    float lv = 0.0f, v[16];
+    auto fetch = [&](int c) {
+        const int rows = seq.len - c * kDeltaChunk;
+        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
+        lk.fetch(kp + t * p.sk.t, p.sk.t, rows, p.K, p.vec_k);
+        lq.fetch(qp + t * p.sq.t, p.sq.t, rows, p.K, p.vec_q);
+        const u32x4 *T0 = reinterpret_cast<const u32x4 *>(p.ws.T + rec * kTri);
+        const u32x4 *P0 = reinterpret_cast<const u32x4 *>(p.ws.P + rec * kTri);
+#pragma unroll
+        for (int i = 0; i < kTriLoads; ++i) {
+            const int at = tid + i * kThreads;
+            if (at < kTri / 8) {
+                lt[i] = T0[at];
+                lp[i] = P0[at];
+            }
+        }
+        lv = p.ws.vec[rec * 256 + tid];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * m + 4 * g + e;
+                v[4 * m + e] = mine && i < rows ? io<T>::load1(vp + (t + i) * p.sv.t) : 0.0f;
+            }
+    };
+    if (chunks > 0) fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+        const int rows = seq.len - c * kDeltaChunk;
+        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
+        __syncthreads();  // the last chunk's reads are done
+        lk.template store<NI>(kt);
+        lq.template store<NI>(qt);
+#pragma unroll
+        for (int i = 0; i < kTriLoads; ++i) {
+            const int at = tid + i * kThreads;
+            if (at < kTri / 8) {
+                reinterpret_cast<u32x4 *>(tt)[at] = lt[i];
+                reinterpret_cast<u32x4 *>(pt)[at] = lp[i];
+            }
+        }
+        vec[tid] = lv;
+        f32x4 X[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) X[m] = f32x4{v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]};
+        __syncthreads();
+        if (c + 1 < chunks) fetch(c + 1);
+
+        if (p.ws.S0) {
+            float *s = p.ws.S0 + rec * KD * p.Vp + col;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+        }
+        // K S and Q S
+        f32x4 ks[4], qs[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) ks[m] = qs[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                Frag<NI> a;
+#pragma unroll
+                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
+                ks[m] = mma<NI, NS>(a, sb, ks[m]);
+#pragma unroll
+                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(qt + n * kTile, 16 * m + r, 4 * b + g);
+                qs[m] = mma<NI, NS>(a, sb, qs[m]);
+            }
+        }
+        // X = beta V - beta e^G K S;  U = X + (T - 1) X
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
+            const f32x4 bt = *reinterpret_cast<const f32x4 *>(vec + 192 + 16 * m + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[m][e] = __builtin_fmaf(bt[e], X[m][e], -be[e] * ks[m][e]);
+        }
+        f32x4 U[4];
+        {
+            const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                U[m] = X[m];
+#pragma unroll
+                for (int b = 0; b <= m / 2; ++b) {
+                    Frag<NS> a;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        a.t[n] = *reinterpret_cast<const bf16x8 *>(tt + ((tri_lower(m, b) * NS + n) * 64 + l) * 8);
+                    U[m] = mma<NS, NS>(a, xb[b], U[m]);
+                }
+            }
+        }
+        if (p.ws.U) {
+            float *u = p.ws.U + rec * 64 * p.Vp + col;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[(long long)(16 * m + 4 * g + e) * p.Vp] = U[m][e];
+        }
+        // Y = scale e^G Q S + P U
+        {
+            const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
+                f32x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = p.scale * eg[e] * qs[m][e];
+#pragma unroll
+                for (int b = 0; b <= m / 2; ++b) {
+                    Frag<NS> a;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        a.t[n] = *reinterpret_cast<const bf16x8 *>(pt + ((tri_lower(m, b) * NS + n) * 64 + l) * 8);
+                    y = mma<NS, NS>(a, ub[b], y);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * m + 4 * g + e;
+                    if (p.y && mine && i < rows) {
+                        const long long at = y0 + (t + i) * p.sy.t;
+                        if (p.out_bf16)
+                            static_cast<bf16_t *>(p.y)[at].bits = uint16_t(pack_bf16x2(y[e], y[e]));
+                        else
+                            static_cast<float *>(p.y)[at] = y[e];
+                    }
+                }
+            }
+        }
+        // S = e^{Gc} S + K^T (e^{Gc - G} U)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
+        }
+        {
+            const Frag<NS> wb[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
+            const float ec = vec[63];
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][e] *= ec;
+                const int col4 = 32 * (m / 2) + 8 * (r & 3) + 4 * (m % 2);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    Frag<NI> a;
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        a.t[n] = read_cols<NCH>(kt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
+                    S[m] = mma<NI, NS>(a, wb[b], S[m]);
+                }
+            }
+        }
+    }
+    if (p.hL && mine) {
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+                if (row < p.K) p.hL[state_at + (long long)row * p.V] = S[m][e];
+            }
+    }
+}
+
+template <typename T, int KD>
+hipError_t prep_kd(const DeltaArgs &a, const PrepParams &p, bool both, hipStream_t stream)
+{
+    const dim3 grid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.h);
+    if (log_enabled())
+        log_line("delta_prep: delta_prep_kernel<in %s, K %d, transposes %d>, grid (%u, %u) x %d threads",
+                 type_tag<T>(), KD, int(both), grid.x, grid.y, kThreads);
+    if (both) delta_prep_kernel<T, KD, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else delta_prep_kernel<T, KD, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int KD>
+hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
+{
+    const dim3 grid((a.V + 63) / 64, a.h, a.nseq);
+    if (log_enabled())
+        log_line("delta_fwd: delta_scan_kernel<in %s, K %d>, grid (%u, %u, %u) x %d threads", type_tag<T>(), KD,
+                 grid.x, grid.y, grid.z, kThreads);
+    delta_scan_kernel<T, KD><<<grid, dim3(kThreads), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaWs &ws, bool both, hipStream_t stream)
+{
+    const int es = a.in_bf16 ? 2 : 4;
+    const PrepParams p{a.seqlen, a.nseq, a.h / a.hk, a.h, a.K, delta_vec(a.q, a.sq, a.K, es, a, a.hk),
+                       delta_vec(a.k, a.sk, a.K, es, a, a.hk), a.scale, a.cu, a.q, a.k, a.g, a.beta,
+                       a.sq, a.sk, a.sg, a.sbeta, ws};
+    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) { return prep_kd<decltype(t), decltype(kd)::value>(a, p, both, stream); });
+}
+
+hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaWs &ws, hipStream_t stream)
+{
+    const int es = a.in_bf16 ? 2 : 4;
+    const ScanParams p{a.seqlen, a.h / a.hk, a.h, a.K, a.V, delta_vp(a.V),
+                       delta_vec(a.q, a.sq, a.K, es, a, a.hk), delta_vec(a.k, a.sk, a.K, es, a, a.hk), a.out_bf16,
+                       a.scale, a.cu, a.q, a.k, a.v, a.h0, a.y, a.hL, a.sq, a.sk, a.sv, a.sy, ws};
+    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) { return scan_kd<decltype(t), decltype(kd)::value>(a, p, stream); });
+}
+
+size_t delta_fwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, int V, int num_seqs)
+{
+    size_t bytes = 0;
+    delta_ws(nullptr, delta_chunks(batch, seqlen, num_seqs) * h, K, V, false, &bytes);
+    return bytes;
+}
+
+hipError_t launch_delta_fwd(const DeltaArgs &a, hipStream_t stream)
+{
+    const long long recs = delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0) * a.h;
+    const DeltaWs ws = delta_ws(a.workspace, recs, a.K, a.V, a.checkpoints, nullptr);
+    const hipError_t e = launch_delta_prep(a, ws, a.checkpoints, stream);
+    return e == hipSuccess ? launch_delta_scan(a, ws, stream) : e;
+}
+
+}  // namespace ssm

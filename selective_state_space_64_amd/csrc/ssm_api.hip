@@ -14,56 +14,14 @@
 
 #include <mutex>
 
+#include "ssm_check.hpp"
 #include "ssm_launch.hpp"
+
+using namespace ssm::check;
 
 namespace {
 
-// True when p is not a multiple of `align` bytes (NULL is never misaligned).
-bool misaligned(const void *p, uintptr_t align)
-{
-    return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0;
-}
-
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Span span(const void *p, size_t bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + bytes};
-}
-
-bool overlaps(const void *p, size_t pb, const void *q, size_t qb)
-{
-    if (!p || !q || pb == 0 || qb == 0) return false;
-    const Span a = span(p, pb), b = span(q, qb);
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-// The value of an enum argument as the int a C caller passed: its bits are
-// read without loading the argument as the enum type, so a value outside the
-// enumeration (an error the validation reports) is not undefined behaviour.
-template <typename E>
-int enum_bits(const E &e)
-{
-    static_assert(sizeof(E) == sizeof(int), "C enums are int-sized");
-    int v = 0;
-    memcpy(&v, &e, sizeof v);
-    return v;
-}
-
-bool valid_dtype(int t) { return t == SSM_F32 || t == SSM_BF16; }
-size_t dsize(int t) { return t == SSM_BF16 ? 2 : 4; }
 bool valid_dstate(int n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
-
-// Product of positive ints as size_t, or 0 on overflow past 2^62.
-size_t mul3(long long a, long long b, long long c)
-{
-    const unsigned __int128 r = (unsigned __int128)a * (unsigned __int128)b * (unsigned __int128)c;
-    if (r > ((unsigned __int128)1 << 62)) return 0;
-    return size_t(r);
-}
 
 // Row stride of strided [batch][rows][seqlen] tensors: 0 means seqlen;
 // false when below seqlen or beyond the kernels' 32-bit in-wave offsets.
