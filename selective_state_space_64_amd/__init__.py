@@ -795,57 +795,156 @@ def ssm_conv1d_update(state, x, weight, *, bias=None, silu=True, out_dtype=None,
     return y
 
 
-def _layout(cls, ts, names, shapes, dtypes):
-    """Pointers and the layout struct `cls` of tensors whose last index (for a
-    shape of 4, or of 3 where `cls` has no head stride) is contiguous.  The
-    dimensions before it are batch, step and (where `cls` has it) head; 0
-    stands for the stride of a dimension of size 1 and of an absent tensor."""
-    fields = [n for n, _ in cls._fields_]
-    order = [n for n in ("batch", "step", "head") if n in fields]
-    out, ptrs = cls(), []
-    for j, (t, name, shape, dtype) in enumerate(zip(ts, names, shapes, dtypes)):
-        if t is None:
-            ptrs.append(None)
+# The calls below check their arguments on (shape, strides, dtype, is_cuda) of
+# each tensor, and keep what follows from those alone (sizes, type codes, the
+# layout struct) for later calls with the same ones: a decode step's host time
+# is then the pointers and one C call.  Addresses are never kept.
+_plan = functools.lru_cache(maxsize=512)
+
+
+def _meta(**tensors):
+    """(name, shape, strides, dtype, is_cuda) of each tensor, None where absent."""
+    try:
+        return tuple([None if t is None else (n, t.shape, t.stride(), t.dtype, t.is_cuda)
+                      for n, t in tensors.items()])
+    except (AttributeError, TypeError):
+        raise TypeError("%s must be CUDA (HIP) tensors" % ", ".join(
+            n for n, t in tensors.items() if t is not None and not isinstance(t, torch.Tensor))) from None
+
+
+def _whole(*metas):
+    """Raise for views that repeat memory (see _no_broadcast)."""
+    for m in metas:
+        if m is not None:
+            for k, (n, st) in enumerate(zip(m[1], m[2])):
+                if n > 1 and st == 0:
+                    raise ValueError("%s is a broadcast view (stride 0 along dimension %d); "
+                                     "pass a materialised tensor (.contiguous())" % (m[0], k))
+
+
+def _expect(m, shape, dtype):
+    if m[1] != torch.Size(shape):
+        raise ValueError("%s has shape %s, expected %s" % (m[0], tuple(m[1]), tuple(shape)))
+    if m[3] != dtype:
+        raise TypeError("%s must be %s, got %s" % (m[0], dtype, m[3]))
+
+
+def _dense(*wanted):
+    """Check (meta, shape, dtype) triples of contiguous tensors (shape None: any
+    shape and dtype)."""
+    for m, shape, dtype in wanted:
+        if m is not None:
+            if shape is not None:
+                _expect(m, shape, dtype)
+            step = 1
+            for n, st in zip(reversed(m[1]), reversed(m[2])):
+                if n > 1 and st != step:
+                    raise ValueError("%s must be contiguous" % m[0])
+                step *= n
+
+
+def _on_gpu(*metas):
+    for m in metas:
+        if m is not None and not m[4]:
+            raise TypeError("%s must be a CUDA (HIP) tensor" % m[0])
+
+
+def _layout(cls, order, *wanted):
+    """The layout struct `cls` of (meta, shape, dtype) triples whose dimension i
+    is order[i] ("batch", "step", "head"); a last index beyond `order` is
+    contiguous.  0 stands for the stride of a dimension of size 1 and of an
+    absent tensor (the library then takes the dense one)."""
+    out = cls()
+    for j, (m, shape, dtype) in enumerate(wanted):
+        if m is None:
             continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-        if t.shape != shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-        if t.dtype != dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        _no_broadcast(t, name)
-        if len(shape) > len(order) and shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError("%s must have a contiguous last index" % name)
-        for d, n in enumerate(order):
-            getattr(out, n)[j] = t.stride(d) if shape[d] > 1 else 0
-        ptrs.append(t.data_ptr())
-    for t, name in zip(ts, names):
-        if t is not None and not t.is_cuda:
-            raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    return ptrs, out
+        _expect(m, shape, dtype)
+        if len(shape) > len(order) and shape[-1] > 1 and m[2][-1] != 1:
+            raise ValueError("%s must have a contiguous last index" % m[0])
+        for d, n in enumerate(order[:len(shape)]):
+            getattr(out, n)[j] = m[2][d] if shape[d] > 1 else 0
+    return out
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _float(v):
     return None if v is None else ctypes.byref(ctypes.c_float(v))
 
 
-def _delta_sizes(q, v, cu_seqlens):
-    if q.dim() != 4 or v.dim() != 4:
+_BTH = ("batch", "step", "head")
+
+
+@_plan
+def _delta_sizes(q, v, cu):
+    if len(q[1]) != 4 or len(v[1]) != 4:
         raise ValueError("q must be [batch, L, qk_heads, K] and v [batch, L, heads, V]")
-    batch, L, hk, K = q.shape
-    nseq = 0
-    if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 2:
-            raise TypeError("cu_seqlens must be an int32 tensor of (sequences + 1) entries")
-        nseq = cu_seqlens.numel() - 1
-    return batch, L, hk, K, v.shape[2], v.shape[3], nseq
+    if cu is not None and (len(cu[1]) != 1 or cu[3] != torch.int32 or cu[1][0] < 2):
+        raise TypeError("cu_seqlens must be an int32 tensor of (sequences + 1) entries")
+    (batch, L, hk, K), (H, V) = q[1], v[1][2:]
+    return batch, L, hk, H, K, V, cu[1][0] - 1 if cu is not None else 0
+
+
+@_plan
+def _delta_fwd_plan(q, k, v, g, beta, y, h0, hL, cu, ws, out_dtype):
+    every = (q, k, v, g, beta, y, h0, hL, cu, ws)
+    _whole(*every)
+    sizes = batch, L, hk, H, K, V, nseq = _delta_sizes(q, v, cu)
+    ind, f32, state = v[3], torch.float32, (nseq or batch, H, K, V)
+    out_dtype = y[3] if y is not None else out_dtype or ind
+    qk, vy, gate = (batch, L, hk, K), (batch, L, H, V), (batch, L, H)
+    layout = _layout(DeltaLayout, _BTH, (q, qk, ind), (k, qk, ind), (v, vy, ind), (y, vy, out_dtype),
+                     (g, gate, f32), (beta, gate, f32))
+    _dense((h0, state, f32), (hL, state, f32), (cu, None, None), (ws, None, None))
+    _on_gpu(*every)
+    need = lib().ssm_delta_fwd_workspace_bytes(*sizes)
+    return sizes, _dtype_code(ind), _dtype_code(out_dtype), out_dtype, state, need, ctypes.byref(layout)
+
+
+@_plan
+def _delta_bwd_plan(q, k, v, g, beta, dy, h0, dhL, cu, ws, dq, dk, dv):
+    every = (q, k, v, g, beta, dy, h0, dhL, cu, ws, dq, dk, dv)
+    _whole(*every)
+    sizes = batch, L, hk, H, K, V, nseq = _delta_sizes(q, v, cu)
+    ind, gt, f32, state = v[3], dy[3], torch.float32, (nseq or batch, H, K, V)
+    qk, vy, gate = (batch, L, hk, K), (batch, L, H, V), (batch, L, H)
+    layout = _layout(DeltaBwdLayout, _BTH, (q, qk, ind), (k, qk, ind), (v, vy, ind), (g, gate, f32),
+                     (beta, gate, f32), (dy, vy, gt), (dq, qk, gt), (dk, qk, gt), (dv, vy, gt))
+    _dense((h0, state, f32), (dhL, state, f32), (cu, None, None), (ws, None, None))
+    _on_gpu(*every)
+    return sizes, _dtype_code(ind), _dtype_code(gt), state, ctypes.byref(layout)
+
+
+@_plan
+def _delta_update_plan(state, q, k, v, g, beta, y, slots, out_dtype):
+    every = (state, q, k, v, g, beta, y, slots)
+    _whole(*every)
+    if len(q[1]) != 3 or len(v[1]) != 3 or len(state[1]) != 4:
+        raise ValueError("q must be [batch, qk_heads, K], v [batch, heads, V], state [slots, heads, K, V]")
+    (batch, hk, K), (H, V) = q[1], v[1][1:]
+    ind, f32 = v[3], torch.float32
+    out_dtype = y[3] if y is not None else out_dtype or ind
+    if slots is None and state[1][0] != batch:
+        raise ValueError("state has %d entries for %d rows (pass slots)" % (state[1][0], batch))
+    qk, vy, gate = (batch, hk, K), (batch, H, V), (batch, H)
+    layout = _layout(DeltaLayout, ("batch", "head"), (q, qk, ind), (k, qk, ind), (v, vy, ind), (y, vy, out_dtype),
+                     (g, gate, f32), (beta, gate, f32))
+    _dense((state, (state[1][0], H, K, V), f32), (slots, (batch,), torch.int32))
+    _on_gpu(*every)
+    return ((batch, hk, H, K, V, _dtype_code(ind)), state[1][0], _dtype_code(out_dtype), out_dtype, vy,
+            ctypes.byref(layout))
 
 
 def ssm_delta_bwd_workspace(q, v, *, cu_seqlens=None):
     """A device buffer of ssm_delta_bwd_workspace_bytes(...) bytes for these
     inputs: `checkpoints` of ssm_delta_fwd and `workspace` of ssm_delta_bwd."""
-    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
-    need = lib().ssm_delta_bwd_workspace_bytes(batch, L, hk, H, K, V, nseq)
+    need = lib().ssm_delta_bwd_workspace_bytes(*_delta_sizes(*_meta(q=q, v=v, cu_seqlens=cu_seqlens)))
     return torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
 
 
@@ -862,31 +961,20 @@ def ssm_delta_fwd(q, k, v, g, beta, *, scale=None, h0=None, cu_seqlens=None, out
     cu_seqlens: int32 device tensor of sequence bounds for sequences packed
     into one batch row.  checkpoints: a buffer from ssm_delta_bwd_workspace
     that receives what ssm_delta_bwd reads (checkpoints_in_workspace=True)."""
-    _no_broadcast_args(q=q, k=k, v=v, g=g, beta=beta, h0=h0, y=y, hL=hL)
-    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
-    ind, f32, dev = v.dtype, torch.float32, v.device
-    out_dtype = y.dtype if y is not None else (out_dtype or ind)
-    state = (nseq or batch, H, K, V)
+    ws = checkpoints if checkpoints is not None else workspace
+    sizes, code, out_code, out_dtype, state, need, layout = _delta_fwd_plan(
+        *_meta(q=q, k=k, v=v, g=g, beta=beta, y=y, h0=h0, hL=hL, cu_seqlens=cu_seqlens, workspace=ws), out_dtype)
+    dev = v.device
     if y is None:
-        y = torch.empty((batch, L, H, V), dtype=out_dtype, device=dev)
+        y = torch.empty(v.shape, dtype=out_dtype, device=dev)
     if hL is None and return_final_state:
-        hL = torch.empty(state, dtype=f32, device=dev)
-    (qp, kp, vp, yp, gp, bp), layout = _layout(
-        DeltaLayout, (q, k, v, y, g, beta), ("q", "k", "v", "y", "g", "beta"),
-        ((batch, L, hk, K), (batch, L, hk, K), (batch, L, H, V), (batch, L, H, V), (batch, L, H), (batch, L, H)),
-        (ind, ind, ind, out_dtype, f32, f32))
-    flags, ws = 0, workspace
-    if checkpoints is not None:
-        flags, ws = SSM_FLAG_CHECKPOINTS, checkpoints
-    elif ws is None:
-        need = lib().ssm_delta_fwd_workspace_bytes(batch, L, hk, H, K, V, nseq)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = lib().ssm_delta_fwd(
-        batch, L, hk, H, K, V, _dtype_code(ind), flags, _float(scale), qp, kp, vp,
-        gp, bp, _ptr(h0, "h0", state, f32), _ptr(cu_seqlens, "cu_seqlens"), nseq, _dtype_code(out_dtype), yp,
-        _ptr(hL, "hL", state, f32), _ptr(ws, "workspace"),
-        0 if ws is None else ws.numel() * ws.element_size(), ctypes.byref(layout), _stream(stream, dev))
-    _check(st)
+        hL = torch.empty(state, dtype=torch.float32, device=dev)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().ssm_delta_fwd(
+        *sizes[:6], code, SSM_FLAG_CHECKPOINTS if checkpoints is not None else 0, _float(scale), q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _at(h0), _at(cu_seqlens), sizes[6], out_code,
+        y.data_ptr(), _at(hL), _at(ws), _bytes(ws), layout, _stream(stream, dev)))
     return y, hL
 
 
@@ -898,31 +986,24 @@ def ssm_delta_bwd(q, k, v, g, beta, dy, *, scale=None, h0=None, dhL=None, cu_seq
     dg, dbeta and dh0 (fp32).  workspace: from ssm_delta_bwd_workspace
     (allocated here when not given); checkpoints_in_workspace=True when
     ssm_delta_fwd filled it for the same inputs."""
-    _no_broadcast_args(q=q, k=k, v=v, g=g, beta=beta, dy=dy, h0=h0, dhL=dhL, dq=dq, dk=dk, dv=dv)
-    batch, L, hk, K, H, V, nseq = _delta_sizes(q, v, cu_seqlens)
-    ind, gt, f32, dev = v.dtype, dy.dtype, torch.float32, v.device
-    state = (nseq or batch, H, K, V)
+    sizes, code, g_code, state, layout = _delta_bwd_plan(
+        *_meta(q=q, k=k, v=v, g=g, beta=beta, dy=dy, h0=h0, dhL=dhL, cu_seqlens=cu_seqlens, workspace=workspace,
+               dq=dq, dk=dk, dv=dv))
     if workspace is None:
         if checkpoints_in_workspace:
             raise ValueError("checkpoints_in_workspace needs the workspace that ssm_delta_fwd filled")
         workspace = ssm_delta_bwd_workspace(q, v, cu_seqlens=cu_seqlens)
-    new = lambda t, *shape: torch.empty(shape, dtype=gt, device=dev) if t is None else t  # noqa: E731
-    out = {"dq": new(dq, batch, L, hk, K), "dk": new(dk, batch, L, hk, K), "dv": new(dv, batch, L, H, V),
-           "dg": torch.empty((batch, L, H), dtype=f32, device=dev),
-           "dbeta": torch.empty((batch, L, H), dtype=f32, device=dev),
+    gt, dev, f32 = dy.dtype, v.device, torch.float32
+    out = {"dq": torch.empty(q.shape, dtype=gt, device=dev) if dq is None else dq,
+           "dk": torch.empty(k.shape, dtype=gt, device=dev) if dk is None else dk,
+           "dv": torch.empty(v.shape, dtype=gt, device=dev) if dv is None else dv,
+           "dg": torch.empty(g.shape, dtype=f32, device=dev), "dbeta": torch.empty(g.shape, dtype=f32, device=dev),
            "dh0": torch.empty(state, dtype=f32, device=dev)}
-    qk, vy, gate = (batch, L, hk, K), (batch, L, H, V), (batch, L, H)
-    (qp, kp, vp, gp, bp, dyp, dqp, dkp, dvp), layout = _layout(
-        DeltaBwdLayout, (q, k, v, g, beta, dy, out["dq"], out["dk"], out["dv"]),
-        ("q", "k", "v", "g", "beta", "dy", "dq", "dk", "dv"), (qk, qk, vy, gate, gate, vy, qk, qk, vy),
-        (ind, ind, ind, f32, f32, gt, gt, gt, gt))
-    st = lib().ssm_delta_bwd(
-        batch, L, hk, H, K, V, _dtype_code(ind), SSM_FLAG_CHECKPOINTS if checkpoints_in_workspace else 0,
-        _float(scale), qp, kp, vp, gp, bp, _ptr(h0, "h0", state, f32),
-        _ptr(cu_seqlens, "cu_seqlens"), nseq, _dtype_code(gt), dyp, _ptr(dhL, "dhL", state, f32), dqp, dkp, dvp,
-        _ptr(out["dg"], "dg"), _ptr(out["dbeta"], "dbeta"), _ptr(out["dh0"], "dh0"), _ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), ctypes.byref(layout), _stream(stream, dev))
-    _check(st)
+    _check(lib().ssm_delta_bwd(
+        *sizes[:6], code, SSM_FLAG_CHECKPOINTS if checkpoints_in_workspace else 0, _float(scale), q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _at(h0), _at(cu_seqlens), sizes[6], g_code,
+        dy.data_ptr(), _at(dhL), *[t.data_ptr() for t in out.values()], workspace.data_ptr(), _bytes(workspace),
+        layout, _stream(stream, dev)))
     return out
 
 
@@ -934,28 +1015,13 @@ def ssm_delta_update(state, q, k, v, g, beta, *, scale=None, slots=None, out_dty
     qk_heads, K], v [batch, heads, V], g and beta [batch, heads].  slots:
     int32 device tensor with each row's state (None: row b uses state b; a
     negative or too large slot skips the row, its y is zero)."""
-    _no_broadcast_args(state=state, q=q, k=k, v=v, g=g, beta=beta, y=y)
-    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
-        raise ValueError("q must be [batch, qk_heads, K], v [batch, heads, V], state [slots, heads, K, V]")
-    batch, hk, K = q.shape
-    H, V = v.shape[1:]
-    ind, f32 = v.dtype, torch.float32
-    out_dtype = y.dtype if y is not None else (out_dtype or ind)
+    sizes, num_slots, out_code, out_dtype, shape, layout = _delta_update_plan(
+        *_meta(state=state, q=q, k=k, v=v, g=g, beta=beta, y=y, slots=slots), out_dtype)
     if y is None:
-        y = torch.empty((batch, H, V), dtype=out_dtype, device=v.device)
-    if slots is None and state.shape[0] != batch:
-        raise ValueError("state has %d entries for %d rows (pass slots)" % (state.shape[0], batch))
-    with_step = lambda t: None if t is None else t.unsqueeze(1)  # noqa: E731
-    qk, vy, gate = (batch, 1, hk, K), (batch, 1, H, V), (batch, 1, H)
-    (qp, kp, vp, yp, gp, bp), layout = _layout(
-        DeltaLayout, [with_step(t) for t in (q, k, v, y, g, beta)], ("q", "k", "v", "y", "g", "beta"),
-        (qk, qk, vy, vy, gate, gate), (ind, ind, ind, out_dtype, f32, f32))
-    st = lib().ssm_delta_update(
-        batch, hk, H, K, V, _dtype_code(ind), _float(scale),
-        _ptr(state, "state", (state.shape[0], H, K, V), f32), state.shape[0],
-        _ptr(slots, "slots", (batch,), torch.int32), qp, kp, vp, gp, bp, _dtype_code(out_dtype), yp,
-        ctypes.byref(layout), _stream(stream, v.device))
-    _check(st)
+        y = torch.empty(shape, dtype=out_dtype, device=v.device)
+    _check(lib().ssm_delta_update(
+        *sizes, _float(scale), state.data_ptr(), num_slots, _at(slots), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        g.data_ptr(), beta.data_ptr(), out_code, y.data_ptr(), layout, _stream(stream, v.device)))
     return y
 
 
@@ -964,66 +1030,63 @@ def _norm_flags(rms, silu, gate_first):
             | (SSM_NORM_GATE_FIRST if gate_first else 0))
 
 
-def _norm_3d(t):
-    return t.unsqueeze(1) if isinstance(t, torch.Tensor) and t.dim() == 2 else t
+@_plan
+def _norm_plan(cls, tensors, dtypes, vectors, workspace=None):
+    """Sizes and layout of [batch, L, dim] or [batch, dim] tensors, x the first."""
+    _whole(*tensors, *vectors, workspace)
+    x = tensors[0]
+    if len(x[1]) not in (2, 3):
+        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
+    order = ("batch", "step")[:len(x[1]) - 1]
+    layout = _layout(cls, order, *[(m, x[1], t) for m, t in zip(tensors, dtypes)])
+    dim = x[1][-1]
+    _dense(*[(m, (dim,), torch.float32) for m in vectors], (workspace, None, None))
+    _on_gpu(*tensors, *vectors, workspace)
+    return (x[1][0], x[1][1] if len(x[1]) == 3 else 1, dim), [_dtype_code(t) for t in dtypes], ctypes.byref(layout)
 
 
 @_on_caller_stream
-def ssm_group_norm_fwd(x, groups, *, weight=None, bias=None, z=None, eps=1e-5, rms=False, silu=False,
+def ssm_group_norm_fwd(x, groups, *, weight=None, bias=None, z=None, eps=None, rms=False, silu=False,
                        gate_first=False, out_dtype=None, y=None, stream=None):
     """Norm over groups of channels of one step, with an activation; returns y.
     x, z, y: [batch, L, dim] or [batch, dim] (channels contiguous, step and
     batch strides free); weight, bias [dim] fp32.  a = normalise(x) * weight +
     bias; y = a, silu(a) (silu=True) or a * silu(z) (z given); with gate_first
-    x * silu(z) is normalised and y = a.  rms: no mean is subtracted.
-    out_dtype defaults to x's dtype."""
-    _no_broadcast_args(x=x, weight=weight, bias=bias, z=z, y=y)
-    out_dtype = y.dtype if y is not None else (out_dtype or x.dtype)
+    x * silu(z) is normalised and y = a.  rms: no mean is subtracted.  eps
+    defaults to 1e-5, out_dtype to x's dtype."""
+    m = _meta(x=x, z=z, y=y, weight=weight, bias=bias)
+    ind = x.dtype
+    out_dtype = y.dtype if y is not None else (out_dtype or ind)
+    sizes, codes, layout = _norm_plan(NormLayout, m[:3], (ind, ind, out_dtype), m[3:])
     if y is None:
         y = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    x3, z3, y3 = _norm_3d(x), _norm_3d(z), _norm_3d(y)
-    if x3.dim() != 3:
-        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
-    batch, L, dim = x3.shape
-    (xp, zp, yp), layout = _layout(NormLayout, (x3, z3, y3), ("x", "z", "y"), (x3.shape,) * 3,
-                                   (x.dtype, x.dtype, out_dtype))
-    st = lib().ssm_group_norm_fwd(
-        batch, L, dim, groups, _dtype_code(x.dtype), _norm_flags(rms, silu, gate_first), _float(eps), xp,
-        _ptr(weight, "weight", (dim,), torch.float32), _ptr(bias, "bias", (dim,), torch.float32), zp,
-        _dtype_code(out_dtype), yp, ctypes.byref(layout), _stream(stream, x.device))
-    _check(st)
+    _check(lib().ssm_group_norm_fwd(
+        *sizes, groups, codes[0], _norm_flags(rms, silu, gate_first), _float(eps), x.data_ptr(), _at(weight),
+        _at(bias), _at(z), codes[2], y.data_ptr(), layout, _stream(stream, x.device)))
     return y
 
 
 @_on_caller_stream
-def ssm_group_norm_bwd(x, groups, dy, *, weight=None, bias=None, z=None, eps=1e-5, rms=False, silu=False,
+def ssm_group_norm_bwd(x, groups, dy, *, weight=None, bias=None, z=None, eps=None, rms=False, silu=False,
                        gate_first=False, dx=None, dz=None, workspace=None, stream=None):
     """Gradients of ssm_group_norm_fwd; returns a dict with dx, dz (None without
     z), dweight and dbias (None where weight or bias is not given).  dx and dz
     have dy's dtype, dweight and dbias are fp32."""
-    _no_broadcast_args(x=x, weight=weight, bias=bias, z=z, dy=dy, dx=dx, dz=dz)
-    gt, dev, f32 = dy.dtype, x.device, torch.float32
+    m = _meta(x=x, z=z, dy=dy, dx=dx, dz=dz, weight=weight, bias=bias, workspace=workspace)
+    ind, gt, dev, f32 = x.dtype, dy.dtype, x.device, torch.float32
+    sizes, codes, layout = _norm_plan(NormBwdLayout, m[:5], (ind, ind, gt, gt, gt), m[5:7], m[7])
     dx = torch.empty(x.shape, dtype=gt, device=dev) if dx is None else dx
     if z is not None and dz is None:
         dz = torch.empty(x.shape, dtype=gt, device=dev)
-    ts = [_norm_3d(t) for t in (x, z, dy, dx, dz)]
-    if ts[0].dim() != 3:
-        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
-    batch, L, dim = ts[0].shape
-    dw = torch.empty(dim, dtype=f32, device=dev) if weight is not None else None
-    db = torch.empty(dim, dtype=f32, device=dev) if bias is not None else None
+    dw = torch.empty(sizes[2], dtype=f32, device=dev) if weight is not None else None
+    db = torch.empty(sizes[2], dtype=f32, device=dev) if bias is not None else None
     if workspace is None and (dw is not None or db is not None):
-        need = lib().ssm_group_norm_bwd_workspace_bytes(batch, L, dim, groups)
+        need = lib().ssm_group_norm_bwd_workspace_bytes(*sizes, groups)
         workspace = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
-    (xp, zp, dyp, dxp, dzp), layout = _layout(NormBwdLayout, ts, ("x", "z", "dy", "dx", "dz"),
-                                              (ts[0].shape,) * 5, (x.dtype, x.dtype, gt, gt, gt))
-    st = lib().ssm_group_norm_bwd(
-        batch, L, dim, groups, _dtype_code(x.dtype), _norm_flags(rms, silu, gate_first), _float(eps), xp,
-        _ptr(weight, "weight", (dim,), f32), _ptr(bias, "bias", (dim,), f32), zp, _dtype_code(gt), dyp, dxp, dzp,
-        _ptr(dw, "dweight"), _ptr(db, "dbias"), _ptr(workspace, "workspace"),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), ctypes.byref(layout),
-        _stream(stream, dev))
-    _check(st)
+    _check(lib().ssm_group_norm_bwd(
+        *sizes, groups, codes[0], _norm_flags(rms, silu, gate_first), _float(eps), x.data_ptr(), _at(weight),
+        _at(bias), _at(z), codes[2], dy.data_ptr(), dx.data_ptr(), _at(dz), _at(dw), _at(db), _at(workspace),
+        _bytes(workspace), layout, _stream(stream, dev)))
     return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
 
 

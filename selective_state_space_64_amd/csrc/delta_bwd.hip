@@ -41,7 +41,6 @@ template <typename TG> __device__ inline void store_grad(TG *p, float v)
 // ------------------------------------------------------------ the recurrence
 struct ScanBwdParams {
     int seqlen, rep, h, K, V, Vp;
-    int vec_q, vec_k;
     float scale;
     const int *cu;
     const void *q, *k, *dy;
@@ -52,27 +51,31 @@ struct ScanBwdParams {
     DeltaWs ws;
 };
 
-template <typename T, typename TG, int KD>
-__global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdParams p)
+template <typename T, typename TG, int KD, int kWaves, bool kFast>
+__global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_bwd_kernel(const ScanBwdParams p)
 {
-    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NG = kGradTerms<T, TG, KD>;
-    constexpr int NCH = KD / 8, kTile = 64 * KD, KB = KD / 32;
-    constexpr int kTri = kTriFrags * NS * 512, kTriLoads = (kTri / 8 + kThreads - 1) / kThreads;
-    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile], tt[kTri], pt[kTri];
-    __shared__ __align__(16) float vec[256];
+    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>;
+    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, true>;
+    constexpr int NI = Stage::NI, NS = Stage::NS, NG = kGradTerms<T, TG, KD>;
+    constexpr int NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
+    constexpr int kKept = (KB + 2) * NS;  // stores of a chunk beside dv's 16
+    __shared__ __align__(16) uint16_t lds[Stage::kBuffers * Stage::kBuffer];
 
-    const int head = int(blockIdx.y), tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63;
-    const int r = l & 15, g = l >> 4;
-    const int col = int(blockIdx.x) * 64 + 16 * wave + r;
-    const bool mine = col < p.V;
+    const int head = int(blockIdx.y), l = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), r = l & 15, g = l >> 4;
+    const int col_tile = int(blockIdx.x) * kWaves + wave, col = 16 * col_tile + r;
+    const bool mine = col < p.V, kept = 16 * col_tile < p.Vp;  // the record has whole tiles up to Vp
     const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
     const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
     const long long state_at = ((long long)blockIdx.z * p.h + head) * p.K * (long long)p.V + col;
+    const long long rec0 = (long long)seq.chunk0 * p.h + head;
 
-    const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h;
-    const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h;
-    const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + seq.first * p.sdy.t + head * p.sdy.h + col;
-    TG *vp = static_cast<TG *>(p.dv) + seq.batch * p.sdv.b + seq.first * p.sdv.t + head * p.sdv.h + col;
+    Stage st;
+    st.init(lds, static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h, p.sk.t,
+            static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h, p.sq.t,
+            p.ws.prep + rec0 * p.ws.prep_stride, p.h * p.ws.prep_stride, seq.len, p.K);
+    const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + seq.first * p.sdy.t + head * p.sdy.h;
+    TG *vp = static_cast<TG *>(p.dv) + seq.batch * p.sdv.b + seq.first * p.sdv.t + head * p.sdv.h;
 
     // dS, laid out as S in the forward
     f32x4 S[KD / 16];
@@ -84,78 +87,62 @@ __global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdP
             S[m][e] = p.dhL && mine && row < p.K ? p.dhL[state_at + (long long)row * p.V] : 0.0f;
         }
 
-    TileLoad<T, NCH, kThreads> lk, lq;
-    u32x4 lt[kTriLoads], lp[kTriLoads];
-    float lv = 0.0f, dy[16];
+    Column<TG, kFast> lc;
     auto fetch = [&](int c) {
-        const int rows = seq.len - c * kDeltaChunk;
-        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
-        lk.fetch(kp + t * p.sk.t, p.sk.t, rows, p.K, p.vec_k);
-        lq.fetch(qp + t * p.sq.t, p.sq.t, rows, p.K, p.vec_q);
-        const u32x4 *T0 = reinterpret_cast<const u32x4 *>(p.ws.Tt + rec * kTri);
-        const u32x4 *P0 = reinterpret_cast<const u32x4 *>(p.ws.Pt + rec * kTri);
-#pragma unroll
-        for (int i = 0; i < kTriLoads; ++i) {
-            const int at = tid + i * kThreads;
-            if (at < kTri / 8) {
-                lt[i] = T0[at];
-                lp[i] = P0[at];
-            }
-        }
-        lv = p.ws.vec[rec * 256 + tid];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * m + 4 * g + e;
-                dy[4 * m + e] = mine && i < rows ? io<TG>::load1(yp + (t + i) * p.sdy.t) : 0.0f;
-            }
+        st.start(c);
+        const long long t = (long long)c * kDeltaChunk;
+        lc.fetch(yp + t * p.sdy.t, p.sdy.t, seq.len - c * kDeltaChunk, g, col, mine);
     };
     if (chunks > 0) fetch(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
         const int rows = seq.len - c * kDeltaChunk;
-        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
-        __syncthreads();  // the last chunk's reads are done
-        lk.template store<NI>(kt);
-        lq.template store<NI>(qt);
-#pragma unroll
-        for (int i = 0; i < kTriLoads; ++i) {
-            const int at = tid + i * kThreads;
-            if (at < kTri / 8) {
-                reinterpret_cast<u32x4 *>(tt)[at] = lt[i];
-                reinterpret_cast<u32x4 *>(pt)[at] = lp[i];
-            }
+        const long long t = (long long)c * kDeltaChunk, rec = rec0 + (long long)c * p.h;
+        if constexpr (kAsync) {  // all but the stores that the last chunk made behind the copies
+            if (c == chunks - 1) wait_loads<0>();
+            else if (!kept) wait_loads<16>();
+            else wait_loads<kKept + 16>();
         }
-        vec[tid] = lv;
+        st.store(c);
         f32x4 Y[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) Y[m] = f32x4{dy[4 * m], dy[4 * m + 1], dy[4 * m + 2], dy[4 * m + 3]};
-        __syncthreads();
+        for (int m = 0; m < 4; ++m) Y[m] = lc.tile(m, rows, g, mine);
         if (c > 0) fetch(c - 1);
+        const uint16_t *kt = st.k_tile(c), *qt = st.q_tile(c), *tt = st.first(c), *pt = st.second(c);
+        const float *vec = st.vec(c);
 
-        {
-            float *s = p.ws.dS1 + rec * KD * p.Vp + col;
-#pragma unroll
-            for (int m = 0; m < KD / 16; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
-        }
-        // dU = P^T dY + tail (K dS)
+        // dU = P^T dY + tail (K dS); fragments are read a phase ahead, as in the forward
         f32x4 U[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) U[m] = f32x4{0, 0, 0, 0};
+        Frag<NI> ka[2][4];
+        Frag<NS> tf[kTriFrags], pf[kTriFrags];
+        auto read_k = [&](int b) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NI; ++n)
+                    ka[b & 1][m].t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
+        };
+        auto read_tri = [&](const uint16_t *from, Frag<NS> *to) {
+#pragma unroll
+            for (int i = 0; i < kTriFrags; ++i)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    to[i].t[n] = *reinterpret_cast<const bf16x8 *>(from + ((i * NS + n) * 64 + l) * 8);
+        };
+        read_k(0);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
+            if (b + 1 < KB) read_k(b + 1);
+            else read_tri(pt, pf);
             const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+            if (kept) record_store<NS, KB>(p.ws.dS1 + rec * NS * p.ws.state, col_tile, b, sb);
+            fence();
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                Frag<NI> a;
-#pragma unroll
-                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
-                U[m] = mma<NI, NS>(a, sb, U[m]);
-            }
+            for (int m = 0; m < 4; ++m) U[m] = mma<NI, NS>(ka[b & 1][m], sb, U[m]);
+            fence();
         }
+        read_tri(tt, tf);
         {
             const Frag<NG> yb[2] = {split8<NG>(Y[0], Y[1]), split8<NG>(Y[2], Y[3])};
 #pragma unroll
@@ -163,45 +150,54 @@ __global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdP
                 const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
-#pragma unroll
-                for (int b = m / 2; b < 2; ++b) {
-                    Frag<NS> a;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        a.t[n] = *reinterpret_cast<const bf16x8 *>(pt + ((tri_upper(m, b) * NS + n) * 64 + l) * 8);
-                    U[m] = mma<NS, NG>(a, yb[b], U[m]);
-                }
             }
+            fence();
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int b = m / 2; b < 2; ++b) U[m] = mma<NS, NG>(pf[tri_upper(m, b)], yb[b], U[m]);
+            fence();
         }
         // dX = dU + (T - 1)^T dU
+        Frag<NI> qc[2][2][2], kc[2][2][2];  // Q^T, K^T: [step parity][tile of the pair][time block]
+        auto read_qk = [&](int b) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NI; ++n) {
+                        const int col4 = 32 * b + 8 * (r & 3) + 4 * o;
+                        qc[b & 1][o][i].t[n] = read_cols<NCH>(qt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g, col4);
+                        kc[b & 1][o][i].t[n] = read_cols<NCH>(kt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g, col4);
+                    }
+        };
+        read_qk(0);
         f32x4 X[4];
         {
             const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
+            fence();
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 X[m] = U[m];
 #pragma unroll
-                for (int b = m / 2; b < 2; ++b) {
-                    Frag<NS> a;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        a.t[n] = *reinterpret_cast<const bf16x8 *>(tt + ((tri_upper(m, b) * NS + n) * 64 + l) * 8);
-                    X[m] = mma<NS, NS>(a, ub[b], X[m]);
-                }
+                for (int b = m / 2; b < 2; ++b) X[m] = mma<NS, NS>(tf[tri_upper(m, b)], ub[b], X[m]);
             }
+            fence();
         }
         {
-            float *x = p.ws.dX + rec * 64 * p.Vp + col;
+            if (kept) {
+                record_store<NS, 2>(p.ws.dX + rec * NS * p.ws.step, col_tile, 0, split8<NS>(X[0], X[1]));
+                record_store<NS, 2>(p.ws.dX + rec * NS * p.ws.step, col_tile, 1, split8<NS>(X[2], X[3]));
+            }
+            f32x4 dv[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const f32x4 bt = *reinterpret_cast<const f32x4 *>(vec + 192 + 16 * m + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * m + 4 * g + e;
-                    x[(long long)i * p.Vp] = X[m][e];
-                    if (mine && i < rows) store_grad(vp + (t + i) * p.sdv.t, bt[e] * X[m][e]);
-                }
+                for (int e = 0; e < 4; ++e) dv[m][e] = bt[e] * X[m][e];
             }
+            store_column<TG, kFast>(vp + t * p.sdv.t, p.sdv.t, rows, g, col, mine, dv);
         }
         // dS = e^{Gc} dS + Q^T (scale e^G dY) - K^T (beta e^G dX)
 #pragma unroll
@@ -219,21 +215,19 @@ __global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdP
             const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
             const float ec = vec[63];
 #pragma unroll
-            for (int m = 0; m < KD / 16; ++m) {
+            for (int b = 0; b < KB; ++b) {
+                if (b + 1 < KB) read_qk(b + 1);
+                fence();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[m][e] *= ec;
-                const int col4 = 32 * (m / 2) + 8 * (r & 3) + 4 * (m % 2);
+                for (int o = 0; o < 2; ++o) {
+                    f32x4 &d = S[2 * b + o];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    Frag<NI> a;
+                    for (int e = 0; e < 4; ++e) d[e] *= ec;
 #pragma unroll
-                    for (int n = 0; n < NI; ++n)
-                        a.t[n] = read_cols<NCH>(qt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
-                    S[m] = mma<NI, NS>(a, yb[b], S[m]);
-#pragma unroll
-                    for (int n = 0; n < NI; ++n)
-                        a.t[n] = read_cols<NCH>(kt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
-                    S[m] = mma<NI, NS>(a, xb[b], S[m]);
+                    for (int i = 0; i < 2; ++i) {
+                        d = mma<NI, NS>(qc[b & 1][o][i], yb[i], d);
+                        d = mma<NI, NS>(kc[b & 1][o][i], xb[i], d);
+                    }
                 }
             }
         }
@@ -252,7 +246,6 @@ __global__ __launch_bounds__(kThreads) void delta_scan_bwd_kernel(const ScanBwdP
 // ------------------------------------------------------------ sums over the value channels
 struct GradParams {
     int seqlen, nseq, rep, h, K, V, Vp;
-    int vec_q, vec_k, vec_v, vec_dy;
     float scale;
     const int *cu;
     const void *q, *k, *v, *dy;
@@ -285,23 +278,41 @@ template <int N> __device__ inline float tile_value(const uint16_t *tile, int pl
     return v;
 }
 
-template <typename T, typename TG, int KD>
-__global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p)
+// Sum of a . b over the lane's 8 elements, both in N terms.
+template <int N> __device__ inline float dot8(const Frag<N> &a, const Frag<N> &b, float s)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j + i < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+                s = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a.t[i][e], a.t[i][e + 1]}, bf16x2{b.t[j][e], b.t[j][e + 1]}, s,
+                                                    false);
+    return s;
+}
+
+// kShared: a key head has several value heads, whose sums meet here.
+template <typename T, typename TG, int KD, bool kShared, bool kFast>
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && KD <= 128 && !kShared ? 2 : 1))
+void delta_grad_kernel(const GradParams p)
 {
     constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NG = kGradTerms<T, TG, KD>;
     constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;  // K and Q are staged KH columns at a time
-    constexpr int kHalves = KD / KH, NT = KH / 64, NTT = KD / 64;           // column tiles of a wave
-    constexpr int VB = sizeof(T) == 2 ? 64 : 32, NCV = VB / 8, kVTile = 64 * VB;
-    constexpr int kStage = (NG + 2 * NS) * kVTile * 2, kZ = 64 * 64, kZs = 2 * NS * kZ * 2, kW = 64 * 68 * 4;
-    constexpr int kUnion = kStage > kZs ? (kStage > kW ? kStage : kW) : (kZs > kW ? kZs : kW);
-    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile];
-    __shared__ __align__(16) unsigned char lds[kUnion];
+    constexpr int kHalves = KD / KH, NT = KH / 64, NTT = KD / 64, KB = KD / 32;  // NTT column tiles a wave
+    // LDS: 32 value columns of S0, dS1, U, dX, dY and V, then K, Q and the 64 x 64 matrices
+    constexpr int kStates = 2 * KB * NS * 512, kSteps = 2 * 2 * NS * 512, kCols = 64 * 32, kZ = 64 * 64;
+    constexpr int kStage = 2 * kStates + 2 * kSteps + (NG + NI) * kCols;
+    constexpr int kMats = 2 * NS * kZ > 64 * 68 * 2 ? 2 * NS * kZ : 64 * 68 * 2;
+    constexpr int kLds = kStage > 2 * NI * kTile + kMats ? kStage : 2 * NI * kTile + kMats;
+    __shared__ __align__(16) uint16_t lds[kLds];
     __shared__ double G[64];
     __shared__ __align__(16) float vec[256];
     __shared__ float rowd[4][3][64], rect[4][64], row_v[64], row_m[64], dots[4];
-    uint16_t *ty = reinterpret_cast<uint16_t *>(lds), *tx = ty + NG * kVTile, *tu = tx + NS * kVTile;
-    uint16_t *zp = reinterpret_cast<uint16_t *>(lds), *zn = zp + NS * kZ;
-    float *W = reinterpret_cast<float *>(lds);
+    uint16_t *ts = lds, *td = ts + kStates, *tu = td + kStates, *tx = tu + kSteps, *ty = tx + kSteps, *tv = ty + NG * kCols;
+    uint16_t *kt = lds, *qt = kt + NI * kTile, *zp = qt + NI * kTile, *zn = zp + NS * kZ;
+    float *W = reinterpret_cast<float *>(zp);
 
     const int chunk = int(blockIdx.x), qk_head = int(blockIdx.y);
     const int si = delta_seq_of(p.cu, p.nseq, p.seqlen, chunk);
@@ -310,32 +321,47 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
     const int rows = min(kDeltaChunk, seq.len - at0);
     if (at0 < 0 || rows <= 0) return;  // the whole workgroup
     const long long t0 = seq.first + at0;
-    const int tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63, r = l & 15, g = l >> 4;
+    const int tid = int(threadIdx.x), l = tid & 63, r = l & 15, g = l >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + t0 * p.sk.t + qk_head * p.sk.h;
     const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + t0 * p.sq.t + qk_head * p.sq.h;
     auto stage_qk = [&](int half) {
-        TileLoad<T, NCH, kThreads> lk, lq;
-        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH, p.vec_k);
-        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH, p.vec_q);
-        lk.template store<NI>(kt);
-        lq.template store<NI>(qt);
+        TileLoad<T, NCH, kThreads, kFast> lk, lq;
+        lk.init(p.sk.t, p.K - half * KH);
+        lq.init(p.sq.t, p.K - half * KH);
+        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH);
+        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH);
+        lk.template store<NI>(kt, rows, p.K - half * KH);
+        lq.template store<NI>(qt, rows, p.K - half * KH);
     };
-    if (kHalves == 1) stage_qk(0);
 
     // column tile n of a wave: keys' entries key(n) + lane's r
     auto key = [&](int n) { return (n / NT) * KH + wave * (KH / 4) + 16 * (n % NT); };
-    f32x4 dq[NTT][4], dk[NTT][4];
+    f32x4 dq[kShared ? NTT : 1][4], dk[kShared ? NTT : 1][4];
+    if constexpr (kShared) {
 #pragma unroll
-    for (int n = 0; n < NTT; ++n)
+        for (int n = 0; n < NTT; ++n)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) dq[n][m] = dk[n][m] = f32x4{0, 0, 0, 0};
+            for (int m = 0; m < 4; ++m) dq[n][m] = dk[n][m] = f32x4{0, 0, 0, 0};
+    }
 
-    for (int hi = 0; hi < p.rep; ++hi) {
+    auto store = [&](const f32x4 (*q)[4], const f32x4 (*k)[4]) {
+        TG *dqp = static_cast<TG *>(p.dq) + seq.batch * p.sdq.b + t0 * p.sdq.t + qk_head * p.sdq.h;
+        TG *dkp = static_cast<TG *>(p.dk) + seq.batch * p.sdk.b + t0 * p.sdk.t + qk_head * p.sdk.h;
+#pragma unroll
+        for (int n = 0; n < NTT; ++n) {
+            const int c = key(n) + r;
+            store_column<TG, kFast>(dqp, p.sdq.t, rows, g, c, c < p.K, q[n]);
+            store_column<TG, kFast>(dkp, p.sdk.t, rows, g, c, c < p.K, k[n]);
+        }
+    };
+
+    for (int hi = 0; hi < (kShared ? p.rep : 1); ++hi) {
         const int head = qk_head * p.rep + hi;
         const long long rec = (long long)chunk * p.h + head;
-        __syncthreads();  // the last head's sums are read
-        vec[tid] = p.ws.vec[rec * 256 + tid];
+        __syncthreads();  // the last head's LDS is read
+        vec[tid] = reinterpret_cast<const float *>(p.ws.prep + rec * p.ws.prep_stride + 2 * tri_size(NS))[tid];
         if (wave == 0) {
             float gi = 0.0f;
             if (l < rows) gi = p.gate[seq.batch * p.sg.b + (t0 + l) * p.sg.t + head * p.sg.h];
@@ -343,95 +369,82 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
         }
         const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + t0 * p.sv.t + head * p.sv.h;
         const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + t0 * p.sdy.t + head * p.sdy.h;
-        const float *U = p.ws.U + rec * 64 * p.Vp, *dX = p.ws.dX + rec * 64 * p.Vp;
-        const float *S0 = p.ws.S0 + rec * KD * p.Vp, *dS1 = p.ws.dS1 + rec * KD * p.Vp;
+        const uint16_t *U = p.ws.U + rec * NS * p.ws.step, *dX = p.ws.dX + rec * NS * p.ws.step;
+        const uint16_t *S0 = p.ws.S0 + rec * NS * p.ws.state, *dS1 = p.ws.dS1 + rec * NS * p.ws.state;
 
-        f32x4 ys[NTT][4], xs[NTT][4], us[NTT][4], dP[4], dM[4];
+        f32x4 ys[NTT][4], xs[NTT][4], us[NTT][4], dP[4], dM[4], xv = {0, 0, 0, 0};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
             for (int n = 0; n < NTT; ++n) ys[n][m] = xs[n][m] = us[n][m] = f32x4{0, 0, 0, 0};
             dP[m] = dM[m] = f32x4{0, 0, 0, 0};
         }
-        constexpr int kPer = TileLoad<T, NCV, kThreads>::kPer;
-        float dot = 0.0f, xv[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) xv[i] = 0.0f;
-        for (int v0 = 0; v0 < p.V; v0 += VB) {
-            TileLoad<TG, NCV, kThreads> ly;
-            TileLoad<float, NCV, kThreads> lx, lu;
-            TileLoad<T, NCV, kThreads> lv;
-            ly.fetch(yp + v0, p.sdy.t, rows, p.V - v0, p.vec_dy);
-            lv.fetch(vp + v0, p.sv.t, rows, p.V - v0, p.vec_v);
-            lx.fetch(dX + v0, p.Vp, 64, VB, true);
-            lu.fetch(U + v0, p.Vp, 64, VB, true);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {  // dX . V of the thread's row
-                float x[8], v[8];
-                io<float>::unpack(lx.raw[i].w[0], x);
-                io<float>::unpack(lx.raw[i].w[1], x + 4);
-#pragma unroll
-                for (int w = 0; w < int(sizeof(T) / 2); ++w) io<T>::unpack(lv.raw[i].w[w], v + w * io<T>::kVec);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) xv[i] = __builtin_fmaf(x[e], v[e], xv[i]);
-            }
-            __syncthreads();  // the last block's reads are done
-            ly.template store<NG>(ty);
-            lx.template store<NS>(tx);
-            lu.template store<NS>(tu);
+        float dot = 0.0f;
+        for (int v0 = 0; v0 < p.V; v0 += 32) {
+            if (v0) __syncthreads();  // the last columns' reads are done
+            const long long tile = v0 / 16;
+            copy_linear<4>(S0 + tile * (kStates / 2), kStates * 2, lds_offset(ts));
+            copy_linear<4>(dS1 + tile * (kStates / 2), kStates * 2, lds_offset(td));
+            copy_linear<4>(U + tile * (kSteps / 2), kSteps * 2, lds_offset(tu));
+            copy_linear<4>(dX + tile * (kSteps / 2), kSteps * 2, lds_offset(tx));
+            TileLoad<TG, 4, kThreads, kFast> ly;
+            TileLoad<T, 4, kThreads, kFast> lv;
+            ly.init(p.sdy.t, p.V - v0);
+            lv.init(p.sv.t, p.V - v0);
+            ly.fetch(yp + v0, p.sdy.t, rows, p.V - v0);
+            lv.fetch(vp + v0, p.sv.t, rows, p.V - v0);
+            ly.template store<NG>(ty, rows, p.V - v0);
+            lv.template store<NI>(tv, rows, p.V - v0);
+            wait_loads<0>();
             __syncthreads();
+
+            // S0 and dS1 as right operands: 32 columns by the wave's key entries
+            Frag<NS> sb[NTT], db[NTT];
 #pragma unroll
-            for (int b = 0; b < VB / 32; ++b) {
-                Frag<NG> ay[4], yw;
-                Frag<NS> ax[4], au[4], xw;
+            for (int n = 0; n < NTT; ++n) {
+                const int k4 = key(n) + 4 * (r & 3);
+                sb[n] = record_cols<NS, KB>(ts, key(n) >> 5, (k4 >> 3) & 3, (k4 >> 2) & 1);
+                db[n] = record_cols<NS, KB>(td, key(n) >> 5, (k4 >> 3) & 3, (k4 >> 2) & 1);
+            }
+            Frag<NG> yw;
+            Frag<NI> vw;
+            const Frag<NS> xw = record_cols<NS, 2>(tx, wave >> 1, r & 3, wave & 1);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+            for (int n = 0; n < NG; ++n) yw.t[n] = read_row<4>(ty + n * kCols, 16 * wave + r, g);
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
-                        ay[m].t[n] = read_row<NCV>(ty + n * kVTile, 16 * m + r, 4 * b + g);
+            for (int n = 0; n < NI; ++n) vw.t[n] = read_row<4>(tv + n * kCols, 16 * wave + r, g);
+            Frag<NG> ay[2];
+            Frag<NS> ax[2], au[2];
+            auto read_a = [&](int m) {
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        ax[m].t[n] = read_row<NCV>(tx + n * kVTile, 16 * m + r, 4 * b + g);
-                        au[m].t[n] = read_row<NCV>(tu + n * kVTile, 16 * m + r, 4 * b + g);
-                    }
+                for (int n = 0; n < NG; ++n) ay[m & 1].t[n] = read_row<4>(ty + n * kCols, 16 * m + r, g);
+                ax[m & 1] = record_cols<NS, 2>(tx, m >> 1, r & 3, m & 1);
+                au[m & 1] = record_cols<NS, 2>(tu, m >> 1, r & 3, m & 1);
+            };
+            read_a(0);
+#pragma unroll
+            for (int n = 0; n < NTT; ++n) dot = dot8<NS>(sb[n], db[n], dot);
+            xv = mma<NS, NI>(xw, vw, xv);  // its diagonal: dX . V
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if (m + 1 < 4) read_a(m + 1);
+                fence();
+                if (m <= wave) {  // row tile `wave` of dY U^T and dX U^T
+                    dP[m] = mma<NG, NS>(yw, au[m & 1], dP[m]);
+                    dM[m] = mma<NS, NS>(xw, au[m & 1], dM[m]);
                 }
-#pragma unroll
-                for (int n = 0; n < NG; ++n) yw.t[n] = read_row<NCV>(ty + n * kVTile, 16 * wave + r, 4 * b + g);
-#pragma unroll
-                for (int n = 0; n < NS; ++n) xw.t[n] = read_row<NCV>(tx + n * kVTile, 16 * wave + r, 4 * b + g);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c <= wave) {  // row tile `wave` of dY U^T and dX U^T
-                        dP[c] = mma<NG, NS>(yw, au[c], dP[c]);
-                        dM[c] = mma<NS, NS>(xw, au[c], dM[c]);
-                    }
 #pragma unroll
                 for (int n = 0; n < NTT; ++n) {
-                    const long long at = (long long)(key(n) + r) * p.Vp + v0 + 32 * b + 8 * g;
-                    const f32x4 s0 = *reinterpret_cast<const f32x4 *>(S0 + at);
-                    const f32x4 s1 = *reinterpret_cast<const f32x4 *>(S0 + at + 4);
-                    const f32x4 d0 = *reinterpret_cast<const f32x4 *>(dS1 + at);
-                    const f32x4 d1 = *reinterpret_cast<const f32x4 *>(dS1 + at + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dot = __builtin_fmaf(s0[e], d0[e], __builtin_fmaf(s1[e], d1[e], dot));
-                    const Frag<NS> sb = split8<NS>(s0, s1), db = split8<NS>(d0, d1);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        ys[n][m] = mma<NG, NS>(ay[m], sb, ys[n][m]);
-                        xs[n][m] = mma<NS, NS>(ax[m], sb, xs[n][m]);
-                        us[n][m] = mma<NS, NS>(au[m], db, us[n][m]);
-                    }
+                    ys[n][m] = mma<NG, NS>(ay[m & 1], sb[n], ys[n][m]);
+                    xs[n][m] = mma<NS, NS>(ax[m & 1], sb[n], xs[n][m]);
+                    us[n][m] = mma<NS, NS>(au[m & 1], db[n], us[n][m]);
                 }
+                fence();
             }
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            float s = xv[i];
-#pragma unroll
-            for (int o = 1; o < NCV; o *= 2) s += __shfl_xor(s, o);
-            if (tid % NCV == 0) row_v[(tid + i * kThreads) / NCV] = s;
-        }
+        for (int e = 0; e < 4; ++e)
+            if (r == 4 * g + e) row_v[16 * wave + r] = xv[e];
 #pragma unroll
         for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
         if (l == 0) dots[wave] = dot;
@@ -442,10 +455,8 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
         for (int m = 0; m < 4; ++m) kk[m] = qk[m] = rq[m] = rr[m] = ru[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
-            if (kHalves > 1) {
-                __syncthreads();
-                stage_qk(half);
-            }
+            __syncthreads();
+            stage_qk(half);
             __syncthreads();
 #pragma unroll
             for (int b = 0; b < KH / 32; ++b) {
@@ -493,7 +504,21 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
                     rowd[wave][2][i] = c;
                 }
             }
-        // dP, N = beta dM, W (the staged tiles are read: W takes their place)
+        // ys and us become the products with S0 and dS1 in dQ and dK
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
+            const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+            const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
+#pragma unroll
+            for (int n = 0; n < NTT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ys[n][m][e] *= p.scale * eg[e];
+                    us[n][m][e] = tail[e] * us[n][m][e] - be[e] * xs[n][m][e];
+                }
+        }
+        // dP, N = beta dM, W
         f32x4 sums = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -596,7 +621,7 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
 #pragma unroll
         for (int half = 0; half < kHalves; ++half) {
             if (kHalves > 1) {
-                __syncthreads();
+                if (half) __syncthreads();
                 stage_qk(half);
             }
             __syncthreads();
@@ -623,8 +648,8 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            dq[half * NT + n][m] = mma<NS, NI>(a, kb[n], dq[half * NT + n][m]);
-                            dk[half * NT + n][m] = mma<NS, NI>(z, kb[n], dk[half * NT + n][m]);
+                            ys[half * NT + n][m] = mma<NS, NI>(a, kb[n], ys[half * NT + n][m]);
+                            us[half * NT + n][m] = mma<NS, NI>(z, kb[n], us[half * NT + n][m]);
                         }
                     }
                     if (b >= m / 2) {  // rows j: dP^T Q and N^T K
@@ -635,44 +660,26 @@ __global__ __launch_bounds__(kThreads) void delta_grad_kernel(const GradParams p
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            dk[half * NT + n][m] = mma<NS, NI>(a, qb[n], dk[half * NT + n][m]);
-                            dk[half * NT + n][m] = mma<NS, NI>(z, kb[n], dk[half * NT + n][m]);
+                            us[half * NT + n][m] = mma<NS, NI>(a, qb[n], us[half * NT + n][m]);
+                            us[half * NT + n][m] = mma<NS, NI>(z, kb[n], us[half * NT + n][m]);
                         }
                     }
                 }
             }
         }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
-            const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
-            const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
+        if constexpr (kShared) {
 #pragma unroll
             for (int n = 0; n < NTT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dq[n][m][e] = __builtin_fmaf(p.scale * eg[e], ys[n][m][e], dq[n][m][e]);
-                    dk[n][m][e] += tail[e] * us[n][m][e] - be[e] * xs[n][m][e];
+                for (int m = 0; m < 4; ++m) {
+                    dq[n][m] += ys[n][m];
+                    dk[n][m] += us[n][m];
                 }
+        } else {
+            store(ys, us);
         }
     }
-    TG *dqp = static_cast<TG *>(p.dq) + seq.batch * p.sdq.b + t0 * p.sdq.t + qk_head * p.sdq.h;
-    TG *dkp = static_cast<TG *>(p.dk) + seq.batch * p.sdk.b + t0 * p.sdk.t + qk_head * p.sdk.h;
-#pragma unroll
-    for (int n = 0; n < NTT; ++n) {
-        const int c = key(n) + r;
-        if (c >= p.K) continue;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * m + 4 * g + e;
-                if (i < rows) {
-                    store_grad(dqp + i * p.sdq.t + c, dq[n][m][e]);
-                    store_grad(dkp + i * p.sdk.t + c, dk[n][m][e]);
-                }
-            }
-    }
+    if constexpr (kShared) store(dq, dk);
 }
 
 template <typename T, typename TG, int KD>
@@ -680,22 +687,36 @@ hipError_t launch_typed(const DeltaBwdArgs &b, const DeltaWs &ws, hipStream_t st
 {
     const DeltaArgs &a = b.f;
     const int es = sizeof(T), gs = sizeof(TG), rep = a.h / a.hk, Vp = delta_vp(a.V);
-    const int vq = delta_vec(a.q, a.sq, a.K, es, a, a.hk), vk = delta_vec(a.k, a.sk, a.K, es, a, a.hk);
-    const ScanBwdParams sp{a.seqlen, rep, a.h, a.K, a.V, Vp, vq, vk, a.scale, a.cu, a.q, a.k, b.dy, b.dhL, b.dv,
+    const bool qk = delta_fast(a.q, a.sq, a.K, es, a, a.hk) && delta_fast(a.k, a.sk, a.K, es, a, a.hk);
+    constexpr long long most = (1ll << 31) / 64 / 4;
+    const bool sfast = qk && b.sdy.t < most && b.sdv.t < most;
+    const bool gfast = qk && delta_fast(a.v, a.sv, a.V, es, a, a.h) && delta_fast(b.dy, b.sdy, a.V, gs, a, a.h) &&
+                       b.sdq.t < most && b.sdk.t < most;
+    const ScanBwdParams sp{a.seqlen, rep, a.h, a.K, a.V, Vp, a.scale, a.cu, a.q, a.k, b.dy, b.dhL, b.dv,
                            b.dh0, a.sq, a.sk, b.sdy, b.sdv, ws};
-    const GradParams gp{a.seqlen, a.nseq, rep, a.h, a.K, a.V, Vp, vq, vk, delta_vec(a.v, a.sv, a.V, es, a, a.h),
-                        delta_vec(b.dy, b.sdy, a.V, gs, a, a.h), a.scale, a.cu, a.q, a.k, a.v, b.dy, a.g, a.beta,
+    const GradParams gp{a.seqlen, a.nseq, rep, a.h, a.K, a.V, Vp, a.scale, a.cu, a.q, a.k, a.v, b.dy, a.g, a.beta,
                         b.dq, b.dk, b.dg, b.dbeta, a.sq, a.sk, a.sv, a.sg, a.sbeta, b.sdy, b.sdq, b.sdk, ws};
-    const dim3 sgrid((a.V + 63) / 64, a.h, a.nseq);
-    const dim3 ggrid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.hk);
+    const bool wide = kDeltaAsync<T, KD> && sfast && delta_wide(a);
+    const int waves = wide ? 8 : 4;
+    const dim3 sgrid((a.V + 16 * waves - 1) / (16 * waves), a.h, a.nseq), sblock(64 * waves);
+    const dim3 ggrid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.hk), gblock(kThreads);
     if (log_enabled())
-        log_line("delta_bwd: delta_scan_bwd_kernel, delta_grad_kernel<in %s, grad %s, K %d>, grids (%u, %u, %u), "
-                 "(%u, %u) x %d threads", type_tag<T>(), type_tag<TG>(), KD, sgrid.x, sgrid.y, sgrid.z, ggrid.x,
-                 ggrid.y, kThreads);
-    delta_scan_bwd_kernel<T, TG, KD><<<sgrid, dim3(kThreads), 0, stream>>>(sp);
+        log_line("delta_bwd: delta_scan_bwd_kernel, delta_grad_kernel<in %s, grad %s, K %d>, fast %d, %d, "
+                 "grids (%u, %u, %u) x %u, (%u, %u) x %u threads", type_tag<T>(), type_tag<TG>(), KD, int(sfast),
+                 int(gfast), sgrid.x, sgrid.y, sgrid.z, sblock.x, ggrid.x, ggrid.y, gblock.x);
+    if (!sfast) {
+        delta_scan_bwd_kernel<T, TG, KD, 4, false><<<sgrid, sblock, 0, stream>>>(sp);
+    } else if (!wide) {
+        delta_scan_bwd_kernel<T, TG, KD, 4, true><<<sgrid, sblock, 0, stream>>>(sp);
+    } else {
+        if constexpr (kDeltaAsync<T, KD>) delta_scan_bwd_kernel<T, TG, KD, 8, true><<<sgrid, sblock, 0, stream>>>(sp);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    delta_grad_kernel<T, TG, KD><<<ggrid, dim3(kThreads), 0, stream>>>(gp);
+    if (rep > 1 && gfast) delta_grad_kernel<T, TG, KD, true, true><<<ggrid, gblock, 0, stream>>>(gp);
+    else if (rep > 1) delta_grad_kernel<T, TG, KD, true, false><<<ggrid, gblock, 0, stream>>>(gp);
+    else if (gfast) delta_grad_kernel<T, TG, KD, false, true><<<ggrid, gblock, 0, stream>>>(gp);
+    else delta_grad_kernel<T, TG, KD, false, false><<<ggrid, gblock, 0, stream>>>(gp);
     return hipGetLastError();
 }
 

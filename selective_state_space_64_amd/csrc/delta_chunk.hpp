@@ -24,33 +24,33 @@ template <typename T, int KD> struct Terms {
 };
 
 struct DeltaWs {
-    float *vec;
-    uint16_t *T, *P, *Tt, *Pt;
-    float *S0, *U, *dS1, *dX;
+    uint16_t *prep;     // prep_stride elements a record
+    long long prep_stride;
+    uint16_t *S0, *U, *dS1, *dX;
+    // elements a record for N terms (the stride; the space is for three)
+    long long state, step;  // for one term
 };
 
 inline DeltaWs delta_ws(void *workspace, long long recs, int K, int V, bool bwd, size_t *bytes)
 {
-    const size_t n = size_t(recs), state = size_t(delta_kd(K)) * delta_vp(V), step = size_t(64) * delta_vp(V);
+    const size_t n = size_t(recs);
+    DeltaWs w{};
+    w.state = (long long)delta_kd(K) * delta_vp(V);
+    w.step = 64ll * delta_vp(V);
+    w.prep_stride = prep_size(3, bwd);  // three terms at most
     char *p = static_cast<char *>(workspace);
     size_t at = 0;
-    auto take = [&](size_t each) {
-        char *r = p ? p + at : nullptr;
-        at += n * each;
+    auto take = [&](long long each) {
+        uint16_t *r = p ? reinterpret_cast<uint16_t *>(p + at) : nullptr;
+        at += n * size_t(each) * sizeof(uint16_t);
         return r;
     };
-    DeltaWs w{};
-    const size_t tri = kTriFrags * 3 * 512 * sizeof(uint16_t);  // three terms at most
-    w.vec = reinterpret_cast<float *>(take(256 * sizeof(float)));
-    w.T = reinterpret_cast<uint16_t *>(take(tri));
-    w.P = reinterpret_cast<uint16_t *>(take(tri));
+    w.prep = take(w.prep_stride);
     if (bwd) {
-        w.Tt = reinterpret_cast<uint16_t *>(take(tri));
-        w.Pt = reinterpret_cast<uint16_t *>(take(tri));
-        w.S0 = reinterpret_cast<float *>(take(state * sizeof(float)));
-        w.U = reinterpret_cast<float *>(take(step * sizeof(float)));
-        w.dS1 = reinterpret_cast<float *>(take(state * sizeof(float)));
-        w.dX = reinterpret_cast<float *>(take(step * sizeof(float)));
+        w.S0 = take(3 * w.state);
+        w.U = take(3 * w.step);
+        w.dS1 = take(3 * w.state);
+        w.dX = take(3 * w.step);
     }
     if (bytes) *bytes = at;
     return w;
@@ -78,6 +78,13 @@ __device__ inline double decay_sums(float g)
     return sum;
 }
 
+// 64 steps of a tensor are one buffer of less than 2^31 bytes, and 16-byte
+// accesses fit its rows (see TileLoad).
+inline bool delta_fast(const void *p, const DeltaStride &s, int n, int esize, const DeltaArgs &a, int heads)
+{
+    return delta_vec(p, s, n, esize, a, heads) && s.t < (1ll << 31) / 64 / esize;
+}
+
 // f(T{}, TG{}, padded K) for the call's types.
 template <typename F>
 hipError_t delta_dispatch(bool in_bf16, bool g_bf16, int K, F &&f)
@@ -91,6 +98,112 @@ hipError_t delta_dispatch(bool in_bf16, bool g_bf16, int K, F &&f)
     if (in_bf16) return g_bf16 ? sized(bf16_t{}, bf16_t{}) : sized(bf16_t{}, 0.0f);
     return g_bf16 ? sized(0.0f, bf16_t{}) : sized(0.0f, 0.0f);
 }
+
+// One chunk's K, Q, two triangular matrices and decays for the kWaves waves of
+// a workgroup.  kAsync (bf16 rows that fit 16-byte accesses): copied straight to
+// LDS into the buffer that the chunk before does not use, so that a whole
+// chunk's work hides the copy.  Otherwise they wait in registers meanwhile (fp32
+// is split into its terms on the way) and there is one buffer.
+// kUpper: the record's second half (vec, Tt, Pt).
+template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper> struct ChunkStage {
+    static constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NCH = KD / 8, kTile = 64 * KD;
+    static constexpr int kThreads = 64 * kWaves, kTri = tri_size(NS), kPart = 2 * kTri + 512;
+    static constexpr int kBuffers = kAsync ? 2 : 1, kBuffer = 2 * NI * kTile + kPart;  // u16 elements
+    static constexpr int kPartLoads = (kPart / 8 + kThreads - 1) / kThreads;
+    static constexpr int kRows = kThreads / NCH;  // rows of one copy of all threads
+    static_assert(!kAsync || (NI == 1 && kFast && kRows % 16 == 0), "rows as they are; the same chunk order in each copy");
+
+    uint16_t *lds;
+    const T *kp, *qp;
+    const uint16_t *prep;  // the record's half
+    long long k_step, q_step, prep_step;
+    int len, K;
+    TileLoad<T, NCH, kThreads, kFast> lk, lq;
+    u32x4 lt[kAsync ? 1 : kPartLoads];
+    uint32_t k_off, q_off;
+
+    // k0, q0: the sequence's first step; rec0: the record of its first chunk,
+    // records of a head rec_step elements apart
+    __device__ inline void init(uint16_t *buffers, const T *k0, long long kst, const T *q0, long long qst,
+                                const uint16_t *rec0, long long rec_step, int length, int n)
+    {
+        lds = buffers;
+        kp = k0;
+        qp = q0;
+        k_step = kst;
+        q_step = qst;
+        prep = rec0 + (kUpper ? 2 * kTri : 0);
+        prep_step = rec_step;
+        len = length;
+        K = n;
+        if constexpr (kAsync) {
+            const int t = int(threadIdx.x) / NCH, c = (chunk_at<NCH>(t, int(threadIdx.x) % NCH) / 8) % NCH;
+            k_off = c * 8 < n ? uint32_t(t * int(kst) + c * 8) * 2u : kOutside;
+            q_off = c * 8 < n ? uint32_t(t * int(qst) + c * 8) * 2u : kOutside;
+        } else {
+            lk.init(kst, n);
+            lq.init(qst, n);
+        }
+    }
+    __device__ inline uint16_t *buffer(int c) const { return lds + (kAsync ? (c & 1) * kBuffer : 0); }
+    __device__ inline const uint16_t *k_tile(int c) const { return buffer(c); }
+    __device__ inline const uint16_t *q_tile(int c) const { return buffer(c) + NI * kTile; }
+    __device__ inline const uint16_t *first(int c) const { return buffer(c) + 2 * NI * kTile + (kUpper ? 512 : 0); }
+    __device__ inline const uint16_t *second(int c) const { return first(c) + kTri; }
+    __device__ inline const float *vec(int c) const
+    {
+        return reinterpret_cast<const float *>(buffer(c) + 2 * NI * kTile + (kUpper ? 0 : 2 * kTri));
+    }
+
+    // Starts chunk c's way here.
+    __device__ inline void start(int c)
+    {
+        const int rows = min(len - c * kDeltaChunk, kDeltaChunk);
+        const T *k = kp + (long long)c * kDeltaChunk * k_step, *q = qp + (long long)c * kDeltaChunk * q_step;
+        const uint16_t *part = prep + c * prep_step;
+        if constexpr (kAsync) {
+            const uint32_t to = lds_offset(buffer(c)) + (threadIdx.x >> 6) * 1024;
+#pragma unroll
+            for (int i = 0; i < 64 / kRows; ++i) {
+                const int left = rows - i * kRows;
+                copy_to_lds(copy_buffer(k + (long long)(i * kRows) * k_step, left * k_step * 2), k_off,
+                            to + i * kThreads * 16);
+                copy_to_lds(copy_buffer(q + (long long)(i * kRows) * q_step, left * q_step * 2), q_off,
+                            to + kTile * 2 + i * kThreads * 16);
+            }
+            copy_linear<kWaves>(part, kPart * 2, lds_offset(buffer(c)) + 4 * kTile);
+        } else {
+            lk.fetch(k, k_step, rows, K);
+            lq.fetch(q, q_step, rows, K);
+#pragma unroll
+            for (int i = 0; i < kPartLoads; ++i) {
+                const int at = int(threadIdx.x) + i * kThreads;
+                if (at < kPart / 8) lt[i] = reinterpret_cast<const u32x4 *>(part)[at];
+            }
+        }
+    }
+    // Chunk c is in its buffer for every wave after this.
+    __device__ inline void store(int c)
+    {
+        if constexpr (!kAsync) {
+            const int rows = len - c * kDeltaChunk;
+            __syncthreads();  // the last chunk's reads are done
+            lk.template store<NI>(buffer(c), rows, K);
+            lq.template store<NI>(buffer(c) + NI * kTile, rows, K);
+#pragma unroll
+            for (int i = 0; i < kPartLoads; ++i) {
+                const int at = int(threadIdx.x) + i * kThreads;
+                if (at < kPart / 8) reinterpret_cast<u32x4 *>(buffer(c) + 2 * NI * kTile)[at] = lt[i];
+            }
+        }
+        __syncthreads();
+    }
+};
+
+// Whether a call's recurrence takes the asynchronous form, and whether with
+// eight waves a workgroup (128 columns) in place of four.
+template <typename T, int KD> constexpr bool kDeltaAsync = sizeof(T) == 2 && KD <= 128;
+inline bool delta_wide(const DeltaArgs &a) { return a.V > 64; }
 
 // Matrices of every chunk (delta_fwd.hip); both: the transposes too.
 hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaWs &ws, bool both, hipStream_t stream);

@@ -26,7 +26,6 @@ constexpr int kThreads = 256;
 // ------------------------------------------------------------ a chunk's matrices
 struct PrepParams {
     int seqlen, nseq, rep, h, K;
-    int vec_q, vec_k;
     float scale;
     const int *cu;
     const void *q, *k;
@@ -74,7 +73,7 @@ __device__ inline void write_tri(const float *m, int diag, uint16_t *out)
     }
 }
 
-template <typename T, int KD, bool kBoth>
+template <typename T, int KD, bool kBoth, bool kFast>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p)
 {
     constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
@@ -92,7 +91,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
     const int at = (chunk - sq.chunk0) * kDeltaChunk;  // the chunk's first step in its sequence
     const int rows = min(kDeltaChunk, sq.len - at);
     if (at < 0 || rows <= 0) return;  // the whole workgroup: a record that no chunk uses
-    const long long rec = (long long)chunk * p.h + head, t0 = sq.first + at;
+    uint16_t *out = p.ws.prep + ((long long)chunk * p.h + head) * p.ws.prep_stride;
+    const long long t0 = sq.first + at;
     const int tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63, r = l & 15, g = l >> 4;
 
     if (wave == 0) {
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
         beta[l] = bi;
         const double last = __shfl(sum, 63);
         const float eg = exp2_hw(float(sum) * kLog2e);
-        float *vec = p.ws.vec + rec * 256;
+        float *vec = reinterpret_cast<float *>(out + 2 * tri_size(NS));
         vec[l] = eg;
         vec[64 + l] = exp2_hw(float(last - sum) * kLog2e);
         vec[128 + l] = bi * eg;
@@ -121,12 +121,14 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
     for (int c = 0; c < 4; ++c) kk[c] = qk[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int half = 0; half < KD / KH; ++half) {
-        TileLoad<T, NCH, kThreads> lk, lq;
-        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH, p.vec_k);
-        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH, p.vec_q);
+        TileLoad<T, NCH, kThreads, kFast> lk, lq;
+        lk.init(p.sk.t, p.K - half * KH);
+        lq.init(p.sq.t, p.K - half * KH);
+        lk.fetch(kp + half * KH, p.sk.t, rows, p.K - half * KH);
+        lq.fetch(qp + half * KH, p.sq.t, rows, p.K - half * KH);
         if (half) __syncthreads();
-        lk.template store<NI>(kt);
-        lq.template store<NI>(qt);
+        lk.template store<NI>(kt, rows, p.K - half * KH);
+        lq.template store<NI>(qt, rows, p.K - half * KH);
         __syncthreads();
 #pragma unroll
         for (int b = 0; b < KH / 32; ++b) {
@@ -204,19 +206,18 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
         }
         __syncthreads();
     }
-    constexpr long long kTri = kTriFrags * NS * 512;
-    write_tri<NS, false>(Tm, 1, p.ws.T + rec * kTri);
-    write_tri<NS, false>(P, 0, p.ws.P + rec * kTri);
+    write_tri<NS, false>(Tm, 1, out);
+    write_tri<NS, false>(P, 0, out + tri_size(NS));
     if constexpr (kBoth) {
-        write_tri<NS, true>(Tm, 1, p.ws.Tt + rec * kTri);
-        write_tri<NS, true>(P, 0, p.ws.Pt + rec * kTri);
+        write_tri<NS, true>(Tm, 1, out + 2 * tri_size(NS) + 512);
+        write_tri<NS, true>(P, 0, out + 3 * tri_size(NS) + 512);
     }
 }
 
 // ------------------------------------------------------------ the recurrence
 struct ScanParams {
     int seqlen, rep, h, K, V, Vp;
-    int vec_q, vec_k, out_bf16;
+    int out_bf16;
     float scale;
     const int *cu;
     const void *q, *k, *v;
@@ -227,27 +228,31 @@ struct ScanParams {
     DeltaWs ws;
 };
 
-template <typename T, int KD>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p)
+// kKeep: leave S0 and U of every chunk in the workspace.
+template <typename T, int KD, int kWaves, bool kKeep, bool kFast>
+__global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_kernel(const ScanParams p)
 {
-    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
-    constexpr int NCH = KD / 8, kTile = 64 * KD, KB = KD / 32;
-    constexpr int kTri = kTriFrags * NS * 512, kTriLoads = (kTri / 8 + kThreads - 1) / kThreads;
-    __shared__ __align__(16) uint16_t kt[NI * kTile], qt[NI * kTile], tt[kTri], pt[kTri];
-    __shared__ __align__(16) float vec[256];
+    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>;
+    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, false>;
+    constexpr int NI = Stage::NI, NS = Stage::NS, NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
+    constexpr int kKept = kKeep ? (KB + 2) * NS : 0;  // stores of a chunk beside y's 16
+    __shared__ __align__(16) uint16_t lds[Stage::kBuffers * Stage::kBuffer];
 
-    const int head = int(blockIdx.y), tid = int(threadIdx.x), wave = tid >> 6, l = tid & 63;
-    const int r = l & 15, g = l >> 4;
-    const int col = int(blockIdx.x) * 64 + 16 * wave + r;
-    const bool mine = col < p.V;
+    const int head = int(blockIdx.y), l = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), r = l & 15, g = l >> 4;
+    const int col_tile = int(blockIdx.x) * kWaves + wave, col = 16 * col_tile + r;
+    const bool mine = col < p.V, kept = 16 * col_tile < p.Vp;  // the record has whole tiles up to Vp
     const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
     const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
     const long long state_at = ((long long)blockIdx.z * p.h + head) * p.K * (long long)p.V + col;
+    const long long rec0 = (long long)seq.chunk0 * p.h + head;
 
-    const T *kp = static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h;
-    const T *qp = static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h;
-    const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + seq.first * p.sv.t + head * p.sv.h + col;
-    const long long y0 = seq.batch * p.sy.b + seq.first * p.sy.t + head * p.sy.h + col;
+    Stage st;
+    st.init(lds, static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h, p.sk.t,
+            static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h, p.sq.t,
+            p.ws.prep + rec0 * p.ws.prep_stride, p.h * p.ws.prep_stride, seq.len, p.K);
+    const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + seq.first * p.sv.t + head * p.sv.h;
+    const long long y0 = seq.batch * p.sy.b + seq.first * p.sy.t + head * p.sy.h;
 
     // S: tiles 2 b and 2 b + 1 hold the rows 32 b + 8 g + {0..3} and + {4..7}
     f32x4 S[KD / 16];
@@ -259,82 +264,72 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p
             S[m][e] = p.h0 && mine && row < p.K ? p.h0[state_at + (long long)row * p.V] : 0.0f;
         }
 
-    TileLoad<T, NCH, kThreads> lk, lq;
-    u32x4 lt[kTriLoads], lp[kTriLoads];
-    float lv = 0.0f, v[16];
-    auto fetch = [&](int c) {
-        const int rows = seq.len - c * kDeltaChunk;
-        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
-        lk.fetch(kp + t * p.sk.t, p.sk.t, rows, p.K, p.vec_k);
-        lq.fetch(qp + t * p.sq.t, p.sq.t, rows, p.K, p.vec_q);
-        const u32x4 *T0 = reinterpret_cast<const u32x4 *>(p.ws.T + rec * kTri);
-        const u32x4 *P0 = reinterpret_cast<const u32x4 *>(p.ws.P + rec * kTri);
-#pragma unroll
-        for (int i = 0; i < kTriLoads; ++i) {
-            const int at = tid + i * kThreads;
-            if (at < kTri / 8) {
-                lt[i] = T0[at];
-                lp[i] = P0[at];
-            }
-        }
-        lv = p.ws.vec[rec * 256 + tid];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * m + 4 * g + e;
-                v[4 * m + e] = mine && i < rows ? io<T>::load1(vp + (t + i) * p.sv.t) : 0.0f;
-            }
-    };
-    if (chunks > 0) fetch(0);
+    Column<T, kFast> lc;
+    if (chunks > 0) {
+        st.start(0);
+        lc.fetch(vp, p.sv.t, seq.len, g, col, mine);
+    }
     for (int c = 0; c < chunks; ++c) {
         const int rows = seq.len - c * kDeltaChunk;
-        const long long t = (long long)c * kDeltaChunk, rec = (long long)(seq.chunk0 + c) * p.h + head;
-        __syncthreads();  // the last chunk's reads are done
-        lk.template store<NI>(kt);
-        lq.template store<NI>(qt);
-#pragma unroll
-        for (int i = 0; i < kTriLoads; ++i) {
-            const int at = tid + i * kThreads;
-            if (at < kTri / 8) {
-                reinterpret_cast<u32x4 *>(tt)[at] = lt[i];
-                reinterpret_cast<u32x4 *>(pt)[at] = lp[i];
-            }
+        const long long t = (long long)c * kDeltaChunk, rec = rec0 + (long long)c * p.h;
+        if constexpr (kAsync) {  // all but the stores that the last chunk made behind the copies
+            if (c == 0 || (!kept && !p.y)) wait_loads<0>();
+            else if (!kept) wait_loads<16>();
+            else if (p.y) wait_loads<kKept + 16>();
+            else wait_loads<kKept>();
         }
-        vec[tid] = lv;
+        st.store(c);
         f32x4 X[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) X[m] = f32x4{v[4 * m], v[4 * m + 1], v[4 * m + 2], v[4 * m + 3]};
-        __syncthreads();
-        if (c + 1 < chunks) fetch(c + 1);
-
-        if (p.ws.S0) {
-            float *s = p.ws.S0 + rec * KD * p.Vp + col;
-#pragma unroll
-            for (int m = 0; m < KD / 16; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+        for (int m = 0; m < 4; ++m) X[m] = lc.tile(m, rows, g, mine);
+        if (c + 1 < chunks) {
+            st.start(c + 1);
+            lc.fetch(vp + (t + kDeltaChunk) * p.sv.t, p.sv.t, rows - kDeltaChunk, g, col, mine);
         }
-        // K S and Q S
+        const uint16_t *kt = st.k_tile(c), *qt = st.q_tile(c), *tt = st.first(c), *pt = st.second(c);
+        const float *vec = st.vec(c);
+
+        // K S and Q S.  Each phase's fragments are read while the phase before
+        // it computes (the fences keep the reads ahead of those products).
         f32x4 ks[4], qs[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) ks[m] = qs[m] = f32x4{0, 0, 0, 0};
+        Frag<NI> ka[2][4], qa[2][4];
+        Frag<NS> tf[kTriFrags], pf[kTriFrags];
+        auto read_kq = [&](int b) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < NI; ++n) {
+                    ka[b & 1][m].t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
+                    qa[b & 1][m].t[n] = read_row<NCH>(qt + n * kTile, 16 * m + r, 4 * b + g);
+                }
+        };
+        auto read_tri = [&](const uint16_t *from, Frag<NS> *to) {
+#pragma unroll
+            for (int i = 0; i < kTriFrags; ++i)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    to[i].t[n] = *reinterpret_cast<const bf16x8 *>(from + ((i * NS + n) * 64 + l) * 8);
+        };
+        read_kq(0);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
+            if (b + 1 < KB) read_kq(b + 1);
+            else read_tri(tt, tf);
             const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+            if constexpr (kKeep)
+                if (kept) record_store<NS, KB>(p.ws.S0 + rec * NS * p.ws.state, col_tile, b, sb);
+            fence();
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                Frag<NI> a;
-#pragma unroll
-                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
-                ks[m] = mma<NI, NS>(a, sb, ks[m]);
-#pragma unroll
-                for (int n = 0; n < NI; ++n) a.t[n] = read_row<NCH>(qt + n * kTile, 16 * m + r, 4 * b + g);
-                qs[m] = mma<NI, NS>(a, sb, qs[m]);
+                ks[m] = mma<NI, NS>(ka[b & 1][m], sb, ks[m]);
+                qs[m] = mma<NI, NS>(qa[b & 1][m], sb, qs[m]);
             }
+            fence();
         }
         // X = beta V - beta e^G K S;  U = X + (T - 1) X
+        read_tri(pt, pf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
@@ -345,55 +340,52 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p
         f32x4 U[4];
         {
             const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
+            fence();
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 U[m] = X[m];
 #pragma unroll
-                for (int b = 0; b <= m / 2; ++b) {
-                    Frag<NS> a;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        a.t[n] = *reinterpret_cast<const bf16x8 *>(tt + ((tri_lower(m, b) * NS + n) * 64 + l) * 8);
-                    U[m] = mma<NS, NS>(a, xb[b], U[m]);
-                }
+                for (int b = 0; b <= m / 2; ++b) U[m] = mma<NS, NS>(tf[tri_lower(m, b)], xb[b], U[m]);
             }
-        }
-        if (p.ws.U) {
-            float *u = p.ws.U + rec * 64 * p.Vp + col;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) u[(long long)(16 * m + 4 * g + e) * p.Vp] = U[m][e];
+            fence();
         }
         // Y = scale e^G Q S + P U
+        Frag<NI> kc[2][2][2];  // K^T: [step parity][tile of the pair][time block]
+        auto read_kc = [&](int b) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NI; ++n)
+                        kc[b & 1][o][i].t[n] = read_cols<NCH>(kt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g,
+                                                              32 * b + 8 * (r & 3) + 4 * o);
+        };
+        read_kc(0);
         {
             const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
+            if constexpr (kKeep)
+                if (kept) {
+                    record_store<NS, 2>(p.ws.U + rec * NS * p.ws.step, col_tile, 0, ub[0]);
+                    record_store<NS, 2>(p.ws.U + rec * NS * p.ws.step, col_tile, 1, ub[1]);
+                }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
-                f32x4 y;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = p.scale * eg[e] * qs[m][e];
-#pragma unroll
-                for (int b = 0; b <= m / 2; ++b) {
-                    Frag<NS> a;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        a.t[n] = *reinterpret_cast<const bf16x8 *>(pt + ((tri_lower(m, b) * NS + n) * 64 + l) * 8);
-                    y = mma<NS, NS>(a, ub[b], y);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * m + 4 * g + e;
-                    if (p.y && mine && i < rows) {
-                        const long long at = y0 + (t + i) * p.sy.t;
-                        if (p.out_bf16)
-                            static_cast<bf16_t *>(p.y)[at].bits = uint16_t(pack_bf16x2(y[e], y[e]));
-                        else
-                            static_cast<float *>(p.y)[at] = y[e];
-                    }
-                }
+                for (int e = 0; e < 4; ++e) qs[m][e] *= p.scale * eg[e];
             }
+            fence();
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int b = 0; b <= m / 2; ++b) qs[m] = mma<NS, NS>(pf[tri_lower(m, b)], ub[b], qs[m]);
+            fence();
+            const long long at = y0 + t * p.sy.t;
+            if (p.y && p.out_bf16)
+                store_column<bf16_t, kFast>(static_cast<bf16_t *>(p.y) + at, p.sy.t, rows, g, col, mine, qs);
+            else if (p.y)
+                store_column<float, kFast>(static_cast<float *>(p.y) + at, p.sy.t, rows, g, col, mine, qs);
         }
         // S = e^{Gc} S + K^T (e^{Gc - G} U)
 #pragma unroll
@@ -406,17 +398,15 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p
             const Frag<NS> wb[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
             const float ec = vec[63];
 #pragma unroll
-            for (int m = 0; m < KD / 16; ++m) {
+            for (int b = 0; b < KB; ++b) {
+                if (b + 1 < KB) read_kc(b + 1);
+                fence();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[m][e] *= ec;
-                const int col4 = 32 * (m / 2) + 8 * (r & 3) + 4 * (m % 2);
+                for (int o = 0; o < 2; ++o) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    Frag<NI> a;
+                    for (int e = 0; e < 4; ++e) S[2 * b + o][e] *= ec;
 #pragma unroll
-                    for (int n = 0; n < NI; ++n)
-                        a.t[n] = read_cols<NCH>(kt + n * kTile, 32 * b + 4 * g, 32 * b + 16 + 4 * g, col4);
-                    S[m] = mma<NI, NS>(a, wb[b], S[m]);
+                    for (int i = 0; i < 2; ++i) S[2 * b + o] = mma<NI, NS>(kc[b & 1][o][i], wb[i], S[2 * b + o]);
                 }
             }
         }
@@ -433,26 +423,38 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const ScanParams p
 }
 
 template <typename T, int KD>
-hipError_t prep_kd(const DeltaArgs &a, const PrepParams &p, bool both, hipStream_t stream)
+hipError_t prep_kd(const DeltaArgs &a, const PrepParams &p, bool both, bool fast, hipStream_t stream)
 {
     const dim3 grid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.h);
     if (log_enabled())
-        log_line("delta_prep: delta_prep_kernel<in %s, K %d, transposes %d>, grid (%u, %u) x %d threads",
-                 type_tag<T>(), KD, int(both), grid.x, grid.y, kThreads);
-    if (both) delta_prep_kernel<T, KD, true><<<grid, dim3(kThreads), 0, stream>>>(p);
-    else delta_prep_kernel<T, KD, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+        log_line("delta_prep: delta_prep_kernel<in %s, K %d, transposes %d, fast %d>, grid (%u, %u) x %d threads",
+                 type_tag<T>(), KD, int(both), int(fast), grid.x, grid.y, kThreads);
+    if (both && fast) delta_prep_kernel<T, KD, true, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else if (both) delta_prep_kernel<T, KD, true, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else if (fast) delta_prep_kernel<T, KD, false, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else delta_prep_kernel<T, KD, false, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int KD, int kWaves, bool kFast>
+hipError_t scan_waves(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
+{
+    const dim3 grid((a.V + 16 * kWaves - 1) / (16 * kWaves), a.h, a.nseq), block(64 * kWaves);
+    if (log_enabled())
+        log_line("delta_fwd: delta_scan_kernel<in %s, K %d, waves %d, keep %d, fast %d>, grid (%u, %u, %u) x %u threads",
+                 type_tag<T>(), KD, kWaves, int(p.ws.S0 != nullptr), int(kFast), grid.x, grid.y, grid.z, block.x);
+    if (p.ws.S0) delta_scan_kernel<T, KD, kWaves, true, kFast><<<grid, block, 0, stream>>>(p);
+    else delta_scan_kernel<T, KD, kWaves, false, kFast><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, int KD>
-hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
+hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, bool fast, hipStream_t stream)
 {
-    const dim3 grid((a.V + 63) / 64, a.h, a.nseq);
-    if (log_enabled())
-        log_line("delta_fwd: delta_scan_kernel<in %s, K %d>, grid (%u, %u, %u) x %d threads", type_tag<T>(), KD,
-                 grid.x, grid.y, grid.z, kThreads);
-    delta_scan_kernel<T, KD><<<grid, dim3(kThreads), 0, stream>>>(p);
-    return hipGetLastError();
+    if (!fast) return scan_waves<T, KD, 4, false>(a, p, stream);
+    if constexpr (kDeltaAsync<T, KD>)
+        if (delta_wide(a)) return scan_waves<T, KD, 8, true>(a, p, stream);
+    return scan_waves<T, KD, 4, true>(a, p, stream);
 }
 
 }  // namespace
@@ -460,19 +462,26 @@ hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
 hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaWs &ws, bool both, hipStream_t stream)
 {
     const int es = a.in_bf16 ? 2 : 4;
-    const PrepParams p{a.seqlen, a.nseq, a.h / a.hk, a.h, a.K, delta_vec(a.q, a.sq, a.K, es, a, a.hk),
-                       delta_vec(a.k, a.sk, a.K, es, a, a.hk), a.scale, a.cu, a.q, a.k, a.g, a.beta,
+    const PrepParams p{a.seqlen, a.nseq, a.h / a.hk, a.h, a.K, a.scale, a.cu, a.q, a.k, a.g, a.beta,
                        a.sq, a.sk, a.sg, a.sbeta, ws};
-    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) { return prep_kd<decltype(t), decltype(kd)::value>(a, p, both, stream); });
+    const bool fast = delta_fast(a.q, a.sq, a.K, es, a, a.hk) && delta_fast(a.k, a.sk, a.K, es, a, a.hk);
+    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) {
+        return prep_kd<decltype(t), decltype(kd)::value>(a, p, both, fast, stream);
+    });
 }
 
 hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaWs &ws, hipStream_t stream)
 {
     const int es = a.in_bf16 ? 2 : 4;
-    const ScanParams p{a.seqlen, a.h / a.hk, a.h, a.K, a.V, delta_vp(a.V),
-                       delta_vec(a.q, a.sq, a.K, es, a, a.hk), delta_vec(a.k, a.sk, a.K, es, a, a.hk), a.out_bf16,
-                       a.scale, a.cu, a.q, a.k, a.v, a.h0, a.y, a.hL, a.sq, a.sk, a.sv, a.sy, ws};
-    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) { return scan_kd<decltype(t), decltype(kd)::value>(a, p, stream); });
+    const ScanParams p{a.seqlen, a.h / a.hk, a.h, a.K, a.V, delta_vp(a.V), a.out_bf16, a.scale, a.cu, a.q, a.k,
+                       a.v, a.h0, a.y, a.hL, a.sq, a.sk, a.sv, a.sy, ws};
+    // the columns of v and y need no 16-byte accesses, only 64 steps in one buffer
+    constexpr long long most = (1ll << 31) / 64 / 4;
+    const bool fast = delta_fast(a.q, a.sq, a.K, es, a, a.hk) && delta_fast(a.k, a.sk, a.K, es, a, a.hk) &&
+                      a.sv.t < most && a.sy.t < most;
+    return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) {
+        return scan_kd<decltype(t), decltype(kd)::value>(a, p, fast, stream);
+    });
 }
 
 size_t delta_fwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, int V, int num_seqs)

@@ -83,6 +83,9 @@ template <int N> __device__ inline Frag<N> split8(f32x4 a, f32x4 b)
     return split8<N>(a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]);
 }
 
+// Keeps the instructions before it before those after it.
+__device__ inline void fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---------------------------------------------------------------- LDS tiles
 // A tile of rows of NCH 16-byte chunks (8 bf16 each); a row's chunks are
 // permuted so that 16 rows' same chunk lie in different banks.
@@ -117,31 +120,42 @@ template <int NCH> __device__ inline bf16x8 read_cols(const uint16_t *tile, int 
 }
 
 // ---------------------------------------------------------------- staging
-// 8 elements of one row as loaded; zeros outside the tensor.
+// 8 elements of one row as loaded.  Loads in flight must not meet a use or a
+// branch of their own, so places outside the tensor are loaded from a place
+// inside it and cleared when the tile is stored.
 template <typename T> struct Raw8 {
     u32x4 w[sizeof(T) / 2];
 };
-template <typename T>
-__device__ inline Raw8<T> load8(const T *row, int c, int n, bool live, bool vec)
+// columns [8 c, 8 c + 8) of the n that exist (n >= 1), element by element
+template <typename T> __device__ inline Raw8<T> load8(const T *row, int c, int n)
 {
     Raw8<T> r;
+    uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) r.w[i] = u32x4{0, 0, 0, 0};
-    if (!live || c * 8 >= n) return r;
-    if (vec) {
+    for (int e = 0; e < 8; ++e) {
+        const T *p = row + min(c * 8 + e, n - 1);
+        if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(*p);
+        else v[e] = p->bits;
+    }
 #pragma unroll
-        for (int i = 0; i < int(sizeof(T) / 2); ++i)
-            r.w[i] = reinterpret_cast<const u32x4 *>(row + c * 8)[i];
-    } else {
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4) r.w[e / 4][e % 4] = v[e];
+        else if (e % 2) r.w[0][e / 2] |= v[e] << 16;
+        else r.w[0][e / 2] = v[e];
+    }
+    return r;
+}
+// Zeros from element `count` on.
+template <typename T> __device__ inline Raw8<T> keep8(Raw8<T> r, int count)
+{
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c * 8 + e < n) {
-                if constexpr (sizeof(T) == 4) {
-                    r.w[e / 4][e % 4] = __float_as_uint(row[c * 8 + e]);
-                } else {
-                    r.w[0][e / 2] |= uint32_t(row[c * 8 + e].bits) << (16 * (e % 2));
-                }
-            }
+    for (int i = 0; i < int(sizeof(T) * 2); ++i) {
+        uint32_t &w = reinterpret_cast<uint32_t *>(r.w)[i];
+        if constexpr (sizeof(T) == 4) {
+            w = i < count ? w : 0u;
+        } else {
+            w = 2 * i + 1 < count ? w : 2 * i < count ? w & 0xffffu : 0u;
+        }
     }
     return r;
 }
@@ -161,32 +175,215 @@ template <typename T, int N> __device__ inline Frag<N> terms8(const Raw8<T> &r)
     }
 }
 
+// Buffer descriptor of `bytes` bytes from p on (p the same in every lane):
+// loads outside give 0, stores outside are dropped; a negative size is empty.
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *p, long long bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, max(int(bytes), 0), 0x00020000);
+}
+constexpr uint32_t kOutside = 0x80000000u;  // past every buffer, also with 2^31 added
+
+// Tensor rows as the kernels walk them.  kFast: 16-byte loads fit every row
+// and 64 steps span less than 2^31 bytes, so that a chunk is one buffer whose
+// bounds stand for the masks of steps and columns, and a lane's offsets are
+// the same in every chunk; otherwise element loads with 64-bit addresses.
+
 // A tile of 64 rows x 8 NCH columns held by kThreads threads on its way from
 // memory to N planes in LDS.
-template <typename T, int NCH, int kThreads> struct TileLoad {
-    static constexpr int kPer = 64 * NCH / kThreads;
+template <typename T, int NCH, int kThreads, bool kFast> struct TileLoad {
+    static constexpr int kPer = 64 * NCH / kThreads, kRows = kThreads / NCH;  // rows of one load of all threads
     Raw8<T> raw[kPer];
-    // rows of `step` elements from p on, `rows` of them and columns [0, n) exist
-    __device__ inline void fetch(const T *p, long long step, int rows, int n, bool vec)
+    uint32_t off;
+    // rows of `step` elements, columns [0, n) exist (n < 1: none)
+    __device__ inline void init(long long step, int n)
     {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = int(threadIdx.x) + i * kThreads, t = at / NCH, c = at % NCH;
-            raw[i] = load8(p + (long long)t * step, c, n, t < rows, vec);
+        if constexpr (kFast) {
+            const int t = int(threadIdx.x) / NCH, c = int(threadIdx.x) % NCH;
+            off = c * 8 < n ? uint32_t(t * int(step) + c * 8) * uint32_t(sizeof(T)) : kOutside;
         }
     }
-    template <int N> __device__ inline void store(uint16_t *tile) const
+    // from p on; rows >= 1
+    __device__ inline void fetch(const T *p, long long step, int rows, int n)
+    {
+        if constexpr (kFast) {
+            // a buffer for each run of rows: the offset in it is the same
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int left = min(rows - i * kRows, kRows);
+                // rows that are not there (left < 1): a negative size
+                const auto buf = buffer_of(p + (long long)(i * kRows) * step, n < 1 ? 0 : left * step * (long long)sizeof(T));
+#pragma unroll
+                for (int w = 0; w < int(sizeof(T) / 2); ++w)
+                    raw[i].w[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off + 16 * w, 0, 0));
+            }
+        } else {
+            if (n < 1) return;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int at = int(threadIdx.x) + i * kThreads, t = at / NCH, c = at % NCH;
+                raw[i] = load8(p + (long long)min(t, rows - 1) * step, c, n);
+            }
+        }
+    }
+    // with the same rows and n
+    __device__ inline Raw8<T> at(int i, int rows, int n) const
+    {
+        if constexpr (kFast) return raw[i];
+        const int a = int(threadIdx.x) + i * kThreads;
+        return keep8(raw[i], a / NCH < rows ? n - a % NCH * 8 : 0);
+    }
+    template <int N> __device__ inline void store(uint16_t *tile, int rows, int n) const
     {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int at = int(threadIdx.x) + i * kThreads, t = at / NCH, c = at % NCH;
-            const Frag<N> f = terms8<T, N>(raw[i]);
+            const int a = int(threadIdx.x) + i * kThreads, t = a / NCH, c = a % NCH;
+            const Frag<N> f = terms8<T, N>(at(i, rows, n));
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 *reinterpret_cast<bf16x8 *>(tile + j * (64 * NCH * 8) + chunk_at<NCH>(t, c)) = f.t[j];
         }
     }
 };
+
+// One column's 16 elements of a 64-step chunk in the order of four D tiles:
+// steps 16 m + 4 g + e.  A buffer for each tile, its bound the last step.
+template <typename T, bool kFast> struct Column {
+    T raw[16];
+    // p: column 0
+    __device__ inline void fetch(const T *p, long long step, int rows, int g, int col, bool live)
+    {
+        if constexpr (kFast) {
+            const uint32_t off = live ? uint32_t(4 * g * int(step) + col) * uint32_t(sizeof(T)) : kOutside;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const auto buf = buffer_of(p + (long long)(16 * m) * step, (long long)min(rows - 16 * m, 16) * step * sizeof(T));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t o = off + uint32_t(e * int(step)) * uint32_t(sizeof(T));
+                    if constexpr (sizeof(T) == 4)
+                        raw[4 * m + e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, o, 0, 0));
+                    else
+                        raw[4 * m + e].bits = __builtin_amdgcn_raw_buffer_load_b16(buf, o, 0, 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                raw[i] = p[(long long)min(16 * (i / 4) + 4 * g + i % 4, rows - 1) * step + (live ? col : 0)];
+        }
+    }
+    __device__ inline f32x4 tile(int m, int rows, int g, bool live) const
+    {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = io<T>::load1(&raw[4 * m + e]);
+            if (!kFast) v[e] = live && 16 * m + 4 * g + e < rows ? v[e] : 0.0f;
+        }
+        return v;
+    }
+};
+
+// Stores one column's steps in the same order.
+template <typename T, bool kFast>
+__device__ inline void store_column(T *p, long long step, int rows, int g, int col, bool live, const f32x4 *v)
+{
+    const uint32_t off = live ? uint32_t(4 * g * int(step) + col) * uint32_t(sizeof(T)) : kOutside;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const auto buf = buffer_of(p + (long long)(16 * m) * step, (long long)min(rows - 16 * m, 16) * step * sizeof(T));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t o = off + uint32_t(e * int(step)) * uint32_t(sizeof(T));
+            if constexpr (!kFast) {
+                const int i = 16 * m + 4 * g + e;
+                if (live && i < rows) {
+                    if constexpr (sizeof(T) == 4) p[(long long)i * step + col] = v[m][e];
+                    else p[(long long)i * step + col].bits = uint16_t(pack_bf16x2(v[m][e], v[m][e]));
+                }
+            } else if constexpr (sizeof(T) == 4) {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[m][e]), buf, o, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b16(uint16_t(pack_bf16x2(v[m][e], v[m][e])), buf, o, 0, 0);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- copies to LDS
+// 64 lanes x 16 bytes from a buffer straight into LDS at byte offset `lds`
+// (+ 16 a lane); places outside the buffer give 0.  The data are there for the
+// wave after wait_loads(), for the workgroup after a barrier behind that.  In
+// asm because the compiler would put a wait for the copy before every later
+// LDS read that it cannot tell apart from the copy's place.
+typedef unsigned int sgpr4 __attribute__((ext_vector_type(4)));
+__device__ inline sgpr4 copy_buffer(const void *p, long long bytes)
+{
+    const unsigned long long a = reinterpret_cast<unsigned long long>(p);
+    return sgpr4{unsigned(a), unsigned(a >> 32) & 0xffffu, unsigned(max(int(bytes), 0)), 0x00020000u};
+}
+__device__ inline uint32_t lds_offset(const void *p)
+{
+    return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
+}
+__device__ inline void copy_to_lds(sgpr4 buf, uint32_t off, uint32_t lds)
+{
+    lds = __builtin_amdgcn_readfirstlane(lds);
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf) : "memory");
+}
+// Until at most N of the wave's vector-memory operations are under way (they
+// end in order).
+template <int N> __device__ inline void wait_loads()
+{
+    static_assert(N < 64, "the counter has 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// `bytes` (a multiple of 1 KB) of memory to LDS, spread over kWaves waves
+template <int kWaves> __device__ inline void copy_linear(const void *p, int bytes, uint32_t lds)
+{
+    const sgpr4 buf = copy_buffer(p, bytes);
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    for (int at = wave * 1024; at < bytes; at += kWaves * 1024)
+        copy_to_lds(buf, uint32_t(at) + (threadIdx.x & 63) * 16, lds + at);
+}
+
+// ---------------------------------------------------------------- records
+// S0, dS1 (K x V), U, dX (64 x V) of a chunk are kept as the B fragments that
+// the recurrences form of them: [16 columns][block of 32 rows][term][lane][8].
+// A lane's place is its own but for one bit, so that reading a fragment across
+// (record_cols) meets every LDS bank once.
+__device__ inline int record_lane(int g, int r) { return g * 16 + (r ^ ((g & 1) << 2)); }
+template <int N, int NB>
+__device__ inline void record_store(uint16_t *rec, int col_tile, int b, const Frag<N> &f)
+{
+    const int l = int(threadIdx.x) & 63;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        *reinterpret_cast<bf16x8 *>(rec + (long long)((col_tile * NB + b) * N + n) * 512 +
+                                    record_lane(l >> 4, l & 15) * 8) = f.t[n];
+}
+// From a record's 32 columns in LDS: the lane's columns 8 g + {0..7} of one row.
+// As in read_cols, each quarter b of 16 lanes hands in the place of four rows,
+// and lane r gets row r % 4 of quarter r / 4's: (block, lane group, half of the
+// lane's 8) name the four rows that this lane's l % 4-th quarter means.
+template <int N, int NB>
+__device__ inline Frag<N> record_cols(const uint16_t *rec, int b, int lg, int half)
+{
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const int l = int(threadIdx.x) & 63, g = l >> 4, a = (l & 15) >> 2;
+    Frag<N> f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint16_t *t = rec + (((g >> 1) * NB + b) * N + n) * 512 + half * 4;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(t + record_lane(lg, 8 * (g & 1) + a) * 8));
+        const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(t + record_lane(lg, 8 * (g & 1) + 4 + a) * 8));
+        f.t[n] = __builtin_bit_cast(bf16x8, s16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+    }
+    return f;
+}
 
 // ---------------------------------------------------------------- chunks
 // The steps of one sequence: `first` in batch row `batch`, `len` of them; its
@@ -218,11 +415,11 @@ __device__ inline int delta_seq_of(const int *cu, int nseq, int seqlen, int chun
     return lo;
 }
 
-// ---------------------------------------------------------------- workspace
+// ---------------------------------------------------------------- a chunk's matrices
 // Per (chunk record, head), in this order:
-//   vec   4 x 64 fp32: e^{G_i}, e^{Gc - G_i}, beta_i e^{G_i}, beta_i
-//   T, P  the chunk's lower-triangular matrices T - 1 and P as A fragments
-//   Tt, Pt, S0, U, dS1, dX  for the backward pass
+//   T, P    the chunk's lower-triangular matrices T - 1 and P as A fragments
+//   vec     4 x 64 fp32: e^{G_i}, e^{Gc - G_i}, beta_i e^{G_i}, beta_i
+//   Tt, Pt  their transposes', for the backward pass
 // A triangular 64 x 64 matrix is 6 fragments of 16 x 32: row tile r, column
 // block b; the columns of a fragment are numbered as two D tiles hold them:
 // lane group g's 8 are 32 b + 4 g + {0..3} and 32 b + 16 + 4 g + {0..3}.
@@ -231,5 +428,8 @@ constexpr int kTriFrags = 6;
 // (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
 __host__ __device__ constexpr int tri_lower(int r, int b) { return r < 2 ? r : r == 2 ? 2 + b : 4 + b; }
 __host__ __device__ constexpr int tri_upper(int r, int b) { return r < 2 ? 2 * r + b : 2 + r; }
+// u16 elements of one, and of the record up to vec and in all, for N terms
+constexpr int tri_size(int n) { return kTriFrags * n * 512; }
+constexpr int prep_size(int n, bool both) { return (both ? 4 : 2) * tri_size(n) + 512; }
 
 }  // namespace ssm
