@@ -55,7 +55,7 @@ template <typename T, typename TG, int KD, int kWaves, bool kFast>
 __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_bwd_kernel(const ScanBwdParams p)
 {
     constexpr bool kAsync = kFast && kDeltaAsync<T, KD>;
-    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, true>;
+    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, true, true>;
     constexpr int NI = Stage::NI, NS = Stage::NS, NG = kGradTerms<T, TG, KD>;
     constexpr int NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
     constexpr int kKept = (KB + 2) * NS;  // stores of a chunk beside dv's 16
@@ -88,8 +88,9 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
         }
 
     Column<TG, kFast> lc;
+    constexpr bool kOther = Stage::kOneTile;  // Q takes K's place at the end of a chunk
     auto fetch = [&](int c) {
-        st.start(c);
+        if (!kOther || c == chunks - 1) st.start(c);
         const long long t = (long long)c * kDeltaChunk;
         lc.fetch(yp + t * p.sdy.t, p.sdy.t, seq.len - c * kDeltaChunk, g, col, mine);
     };
@@ -168,7 +169,8 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 #pragma unroll
                     for (int n = 0; n < NI; ++n) {
                         const int col4 = 32 * b + 8 * (r & 3) + 4 * o;
-                        qc[b & 1][o][i].t[n] = read_cols<NCH>(qt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g, col4);
+                        if constexpr (!kOther)
+                            qc[b & 1][o][i].t[n] = read_cols<NCH>(qt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g, col4);
                         kc[b & 1][o][i].t[n] = read_cols<NCH>(kt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g, col4);
                     }
         };
@@ -225,9 +227,21 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                     for (int e = 0; e < 4; ++e) d[e] *= ec;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        d = mma<NI, NS>(qc[b & 1][o][i], yb[i], d);
+                        if constexpr (!kOther) d = mma<NI, NS>(qc[b & 1][o][i], yb[i], d);
                         d = mma<NI, NS>(kc[b & 1][o][i], xb[i], d);
                     }
+                }
+            }
+            if constexpr (kOther) {
+                st.store_other(c);
+                if (c > 0) st.start(c - 1);
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    read_qk(b);
+#pragma unroll
+                    for (int o = 0; o < 2; ++o)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) S[2 * b + o] = mma<NI, NS>(kc[b & 1][o][i], yb[i], S[2 * b + o]);
                 }
             }
         }
@@ -725,15 +739,14 @@ hipError_t launch_typed(const DeltaBwdArgs &b, const DeltaWs &ws, hipStream_t st
 size_t delta_bwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, int V, int num_seqs)
 {
     size_t bytes = 0;
-    delta_ws(nullptr, delta_chunks(batch, seqlen, num_seqs) * h, K, V, true, &bytes);
+    delta_ws(nullptr, batch, seqlen, h, K, V, num_seqs, true, &bytes);
     return bytes;
 }
 
 hipError_t launch_delta_bwd(const DeltaBwdArgs &b, hipStream_t stream)
 {
     const DeltaArgs &a = b.f;
-    const long long recs = delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0) * a.h;
-    const DeltaWs ws = delta_ws(a.workspace, recs, a.K, a.V, true, nullptr);
+    const DeltaWs ws = delta_ws(a, true);
     if (!b.ckpt_given) {  // the forward, for its records only
         hipError_t e = launch_delta_prep(a, ws, true, stream);
         if (e == hipSuccess) e = launch_delta_scan(a, ws, stream);

@@ -14,26 +14,65 @@ inline int delta_kd(int K) { return K <= 64 ? 64 : K <= 128 ? 128 : 256; }
 inline int delta_vp(int V) { return (V + 63) / 64 * 64; }
 
 // bf16 terms of the inputs (kIn) and of what the kernels form from them
-// (kSum: states, U, T, P, ...).  Two terms leave 2^-17 of a value's size,
-// below what the fp32 sums of a chain of products lose by some factor 10 but
-// 200 times under the rounding of a bf16 output; fp32 inputs take three, except where
-// K > 128 leaves no LDS for them.
+// (kSum: states, U, T, P, ...).  Two terms leave 2^-17 of a value's size, 200
+// times under the rounding of a bf16 output; fp32 inputs take three (2^-25).
 template <typename T, int KD> struct Terms {
-    static constexpr int kIn = sizeof(T) == 2 ? 1 : KD > 128 ? 2 : 3;
-    static constexpr int kSum = sizeof(T) == 2 ? 2 : kIn;
+    static constexpr int kIn = sizeof(T) == 2 ? 1 : 3;
+    static constexpr int kSum = sizeof(T) == 2 ? 2 : 3;
 };
+
+#ifndef DELTA_SPLIT_BELOW
+#define DELTA_SPLIT_BELOW 96
+#endif
+#ifndef DELTA_SPLIT_LEAST
+#define DELTA_SPLIT_LEAST 8
+#endif
+constexpr int kSplitBelow = DELTA_SPLIT_BELOW;  // workgroups of 128 columns
+constexpr int kSplitLeast = DELTA_SPLIT_LEAST;  // chunks
 
 struct DeltaWs {
     uint16_t *prep;     // prep_stride elements a record
     long long prep_stride;
     uint16_t *S0, *U, *dS1, *dX;
-    // elements a record for N terms (the stride; the space is for three)
-    long long state, step;  // for one term
+    // elements a record for one term (the space is for three)
+    long long state, step;
+    // sequence split (delta_split), per segment and head: end states [KD][Vp],
+    // then the states entering the next segment; transfer matrices' terms [KD][KD]
+    float *N;
+    uint16_t *M;
+    int seg_chunks;  // 0: not split
 };
 
-inline DeltaWs delta_ws(void *workspace, long long recs, int K, int V, bool bwd, size_t *bytes)
+// Sequence split: where heads x sequences x 128-column tiles leave most of
+// the 256 compute units without a workgroup, a sequence is cut into segments
+// of seg_chunks chunks.  The recurrence is affine in the state, so each
+// segment but a sequence's last first yields its end state from zero (or h0)
+// and its K x K transfer matrix (the same recurrence on the unit columns, no
+// values), these are composed in order, and then all segments run at once.
+// That is about 2.2 times the work, over 256 / (heads x tiles) times the
+// workgroups.  Sizes only, so that the workspace is known before the call.
+struct DeltaSplit {
+    int seg_chunks, segs;  // segs: an upper bound over all sequences
+};
+inline DeltaSplit delta_split(int batch, int seqlen, int h, int V, int num_seqs)
 {
-    const size_t n = size_t(recs);
+    const long long chunks = delta_chunks(batch, seqlen, num_seqs), nseq = num_seqs ? num_seqs : batch;
+    const long long wgs = (long long)h * ((V + 127) / 128);
+    if (nseq * wgs > kSplitBelow) return {0, 0};
+    const long long want = 256 / wgs;  // segments in all
+    long long seg = (chunks + want - 1) / want;
+    if (seg < kSplitLeast) seg = kSplitLeast;
+    // no sequence of two segments (packed ones may all be short but one)
+    if (chunks < 2 * (num_seqs ? 1 : nseq) * seg) return {0, 0};
+    const long long per = (seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    const long long segs = num_seqs ? chunks / seg + num_seqs : batch * ((per + seg - 1) / seg);
+    return {int(seg), int(segs)};
+}
+
+inline DeltaWs delta_ws(void *workspace, int batch, int seqlen, int h, int K, int V, int num_seqs, bool bwd,
+                        size_t *bytes)
+{
+    size_t n = size_t(delta_chunks(batch, seqlen, num_seqs)) * h;
     DeltaWs w{};
     w.state = (long long)delta_kd(K) * delta_vp(V);
     w.step = 64ll * delta_vp(V);
@@ -52,8 +91,20 @@ inline DeltaWs delta_ws(void *workspace, long long recs, int K, int V, bool bwd,
         w.dS1 = take(3 * w.state);
         w.dX = take(3 * w.step);
     }
+    const DeltaSplit split = delta_split(batch, seqlen, h, V, num_seqs);
+    w.seg_chunks = split.seg_chunks;
+    if (split.segs) {
+        n = size_t(split.segs) * h;
+        w.N = reinterpret_cast<float *>(take(2 * w.state));
+        w.M = take(3ll * delta_kd(K) * delta_kd(K));
+    }
     if (bytes) *bytes = at;
     return w;
+}
+
+inline DeltaWs delta_ws(const DeltaArgs &a, bool bwd)
+{
+    return delta_ws(a.workspace, a.batch, a.seqlen, a.h, a.K, a.V, a.cu ? a.nseq : 0, bwd, nullptr);
 }
 
 // 16-byte accesses fit every row of a tensor with n elements a row.
@@ -85,6 +136,45 @@ inline bool delta_fast(const void *p, const DeltaStride &s, int n, int esize, co
     return delta_vec(p, s, n, esize, a, heads) && s.t < (1ll << 31) / 64 / esize;
 }
 
+// What one workgroup runs through: chunks [c0, c1) of a sequence.
+struct DeltaSegment {
+    int seq, index, c0, c1;
+    bool live;  // there is such a segment (an empty sequence has one)
+    bool last;  // of its sequence
+    DeltaSeq s;
+};
+// Segment z: a whole sequence, or with seg_chunks > 0 a part; packed sequence
+// i's segments are numbered from chunk0 / seg_chunks + i on, as its chunks are
+// (delta_seq).
+__device__ inline DeltaSegment delta_segment(const int *cu, int nseq, int seqlen, int seg_chunks, int z)
+{
+    DeltaSegment d{};
+    const int per = (seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    if (!seg_chunks) {
+        d.seq = z;
+    } else if (!cu) {
+        const int n = (per + seg_chunks - 1) / seg_chunks;
+        d.seq = z / n;
+        d.index = z % n;
+    } else {
+        int lo = 0, hi = nseq - 1;  // the last i whose first segment is at or before z
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (delta_seq(cu, mid, seqlen).chunk0 / seg_chunks + mid <= z) lo = mid;
+            else hi = mid - 1;
+        }
+        d.seq = lo;
+        d.index = z - (delta_seq(cu, lo, seqlen).chunk0 / seg_chunks + lo);
+    }
+    d.s = delta_seq(cu, d.seq, seqlen);
+    const int chunks = (d.s.len + kDeltaChunk - 1) / kDeltaChunk;
+    d.c0 = seg_chunks ? d.index * seg_chunks : 0;
+    d.c1 = seg_chunks ? min(d.c0 + seg_chunks, chunks) : chunks;
+    d.live = d.index == 0 || (d.index > 0 && d.c0 < chunks);
+    d.last = d.c1 == chunks;
+    return d;
+}
+
 // f(T{}, TG{}, padded K) for the call's types.
 template <typename F>
 hipError_t delta_dispatch(bool in_bf16, bool g_bf16, int K, F &&f)
@@ -104,11 +194,15 @@ hipError_t delta_dispatch(bool in_bf16, bool g_bf16, int K, F &&f)
 // LDS into the buffer that the chunk before does not use, so that a whole
 // chunk's work hides the copy.  Otherwise they wait in registers meanwhile (fp32
 // is split into its terms on the way) and there is one buffer.
-// kUpper: the record's second half (vec, Tt, Pt).
-template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper> struct ChunkStage {
+// kUpper: the record's second half (vec, Tt, Pt); !kNeedQ: without Q.
+template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, bool kNeedQ> struct ChunkStage {
     static constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NCH = KD / 8, kTile = 64 * KD;
     static constexpr int kThreads = 64 * kWaves, kTri = tri_size(NS), kPart = 2 * kTri + 512;
-    static constexpr int kBuffers = kAsync ? 2 : 1, kBuffer = 2 * NI * kTile + kPart;  // u16 elements
+    // fp32 keys of over 128 entries leave LDS for one of K and Q at a time: store()
+    // then brings Q (kUpper: K), store_other() the other in its place
+    static constexpr bool kOneTile = NI * KD > 512;
+    static constexpr int kTiles = kOneTile ? 1 : 2;
+    static constexpr int kBuffers = kAsync ? 2 : 1, kBuffer = kTiles * NI * kTile + kPart;  // u16 elements
     static constexpr int kPartLoads = (kPart / 8 + kThreads - 1) / kThreads;
     static constexpr int kRows = kThreads / NCH;  // rows of one copy of all threads
     static_assert(!kAsync || (NI == 1 && kFast && kRows % 16 == 0), "rows as they are; the same chunk order in each copy");
@@ -147,12 +241,12 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper> 
     }
     __device__ inline uint16_t *buffer(int c) const { return lds + (kAsync ? (c & 1) * kBuffer : 0); }
     __device__ inline const uint16_t *k_tile(int c) const { return buffer(c); }
-    __device__ inline const uint16_t *q_tile(int c) const { return buffer(c) + NI * kTile; }
-    __device__ inline const uint16_t *first(int c) const { return buffer(c) + 2 * NI * kTile + (kUpper ? 512 : 0); }
+    __device__ inline const uint16_t *q_tile(int c) const { return buffer(c) + (kTiles - 1) * NI * kTile; }
+    __device__ inline const uint16_t *first(int c) const { return buffer(c) + kTiles * NI * kTile + (kUpper ? 512 : 0); }
     __device__ inline const uint16_t *second(int c) const { return first(c) + kTri; }
     __device__ inline const float *vec(int c) const
     {
-        return reinterpret_cast<const float *>(buffer(c) + 2 * NI * kTile + (kUpper ? 0 : 2 * kTri));
+        return reinterpret_cast<const float *>(buffer(c) + kTiles * NI * kTile + (kUpper ? 0 : 2 * kTri));
     }
 
     // Starts chunk c's way here.
@@ -168,13 +262,14 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper> 
                 const int left = rows - i * kRows;
                 copy_to_lds(copy_buffer(k + (long long)(i * kRows) * k_step, left * k_step * 2), k_off,
                             to + i * kThreads * 16);
-                copy_to_lds(copy_buffer(q + (long long)(i * kRows) * q_step, left * q_step * 2), q_off,
-                            to + kTile * 2 + i * kThreads * 16);
+                if constexpr (kNeedQ)
+                    copy_to_lds(copy_buffer(q + (long long)(i * kRows) * q_step, left * q_step * 2), q_off,
+                                to + kTile * 2 + i * kThreads * 16);
             }
             copy_linear<kWaves>(part, kPart * 2, lds_offset(buffer(c)) + 4 * kTile);
         } else {
             lk.fetch(k, k_step, rows, K);
-            lq.fetch(q, q_step, rows, K);
+            if constexpr (kNeedQ) lq.fetch(q, q_step, rows, K);
 #pragma unroll
             for (int i = 0; i < kPartLoads; ++i) {
                 const int at = int(threadIdx.x) + i * kThreads;
@@ -188,14 +283,24 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper> 
         if constexpr (!kAsync) {
             const int rows = len - c * kDeltaChunk;
             __syncthreads();  // the last chunk's reads are done
-            lk.template store<NI>(buffer(c), rows, K);
-            lq.template store<NI>(buffer(c) + NI * kTile, rows, K);
+            if constexpr (!kOneTile || kUpper || !kNeedQ) lk.template store<NI>(buffer(c), rows, K);
+            if constexpr (kNeedQ && !(kOneTile && kUpper))
+                lq.template store<NI>(buffer(c) + (kTiles - 1) * NI * kTile, rows, K);
 #pragma unroll
             for (int i = 0; i < kPartLoads; ++i) {
                 const int at = int(threadIdx.x) + i * kThreads;
-                if (at < kPart / 8) reinterpret_cast<u32x4 *>(buffer(c) + 2 * NI * kTile)[at] = lt[i];
+                if (at < kPart / 8) reinterpret_cast<u32x4 *>(buffer(c) + kTiles * NI * kTile)[at] = lt[i];
             }
         }
+        __syncthreads();
+    }
+    __device__ inline void store_other(int c)
+    {
+        static_assert(!kAsync && kOneTile && kNeedQ, "both tiles are there");
+        const int rows = len - c * kDeltaChunk;
+        __syncthreads();  // the first tile's reads are done
+        if constexpr (kUpper) lq.template store<NI>(buffer(c), rows, K);
+        else lk.template store<NI>(buffer(c), rows, K);
         __syncthreads();
     }
 };

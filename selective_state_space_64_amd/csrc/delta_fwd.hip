@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
 
 // ------------------------------------------------------------ the recurrence
 struct ScanParams {
-    int seqlen, rep, h, K, V, Vp;
+    int seqlen, nseq, rep, h, K, V, Vp;
     int out_bf16;
     float scale;
     const int *cu;
@@ -228,24 +228,36 @@ struct ScanParams {
     DeltaWs ws;
 };
 
-// kKeep: leave S0 and U of every chunk in the workspace.
-template <typename T, int KD, int kWaves, bool kKeep, bool kFast>
+// What a run of the recurrence leaves: y and hL; beside them S0 and U of every
+// chunk; or only a segment's end state and transfer matrix.
+enum { kPlainRun = 0, kKeepRun = 1, kEndRun = 2 };
+
+template <typename T, int KD, int kWaves, int kRun, bool kFast>
 __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_kernel(const ScanParams p)
 {
-    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>;
-    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, false>;
+    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>, kKeep = kRun == kKeepRun, kEnd = kRun == kEndRun;
+    using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, false, !kEnd>;
     constexpr int NI = Stage::NI, NS = Stage::NS, NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
     constexpr int kKept = kKeep ? (KB + 2) * NS : 0;  // stores of a chunk beside y's 16
     __shared__ __align__(16) uint16_t lds[Stage::kBuffers * Stage::kBuffer];
 
     const int head = int(blockIdx.y), l = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), r = l & 15, g = l >> 4;
-    const int col_tile = int(blockIdx.x) * kWaves + wave, col = 16 * col_tile + r;
-    const bool mine = col < p.V, kept = 16 * col_tile < p.Vp;  // the record has whole tiles up to Vp
-    const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
-    const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
-    const long long state_at = ((long long)blockIdx.z * p.h + head) * p.K * (long long)p.V + col;
+    const DeltaSegment seg = delta_segment(p.cu, p.nseq, p.seqlen, p.ws.seg_chunks, int(blockIdx.z));
+    const DeltaSeq &seq = seg.s;
+    // kEnd: the workgroups behind the value columns run the unit columns
+    const int value_wgs = (p.V + 16 * kWaves - 1) / (16 * kWaves);
+    const bool unit = kEnd && int(blockIdx.x) >= value_wgs;
+    if (!seg.live) return;                                       // the whole workgroup
+    if (kEnd && (seg.last || (unit && seg.index == 0))) return;  // nothing follows, or nothing enters it
+    const int col_tile = (int(blockIdx.x) - (unit ? value_wgs : 0)) * kWaves + wave, col = 16 * col_tile + r;
+    const bool mine = !unit && col < p.V, kept = 16 * col_tile < p.Vp;  // the record has whole tiles up to Vp
+    const int c0 = seg.c0, chunks = seg.c1;
+    const long long state_at = ((long long)seg.seq * p.h + head) * p.K * (long long)p.V + col;
     const long long rec0 = (long long)seq.chunk0 * p.h + head;
+    // this segment's place in N and M, and the state entering it
+    const long long slot = (long long)blockIdx.z * p.h + head;
+    const float *entry = seg.index ? p.ws.N + (slot - p.h) * p.ws.state + col : nullptr;
 
     Stage st;
     st.init(lds, static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h, p.sk.t,
@@ -261,19 +273,24 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
-            S[m][e] = p.h0 && mine && row < p.K ? p.h0[state_at + (long long)row * p.V] : 0.0f;
+            float s = 0.0f;
+            if (kEnd ? seg.index != 0 : false) s = unit && row == col ? 1.0f : 0.0f;
+            else if (entry) s = kept ? entry[(long long)row * p.Vp] : 0.0f;
+            else if (p.h0 && mine && row < p.K) s = p.h0[state_at + (long long)row * p.V];
+            S[m][e] = s;
         }
 
     Column<T, kFast> lc;
-    if (chunks > 0) {
-        st.start(0);
-        lc.fetch(vp, p.sv.t, seq.len, g, col, mine);
+    if (chunks > c0) {
+        const long long t = (long long)c0 * kDeltaChunk;
+        st.start(c0);
+        lc.fetch(vp + t * p.sv.t, p.sv.t, seq.len - c0 * kDeltaChunk, g, col, mine);
     }
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = c0; c < chunks; ++c) {
         const int rows = seq.len - c * kDeltaChunk;
         const long long t = (long long)c * kDeltaChunk, rec = rec0 + (long long)c * p.h;
         if constexpr (kAsync) {  // all but the stores that the last chunk made behind the copies
-            if (c == 0 || (!kept && !p.y)) wait_loads<0>();
+            if (kEnd || c == c0 || (!kept && !p.y)) wait_loads<0>();
             else if (!kept) wait_loads<16>();
             else if (p.y) wait_loads<kKept + 16>();
             else wait_loads<kKept>();
@@ -282,8 +299,9 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
         f32x4 X[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) X[m] = lc.tile(m, rows, g, mine);
+        constexpr bool kOther = Stage::kOneTile && !kEnd;  // K takes Q's place after Q S
         if (c + 1 < chunks) {
-            st.start(c + 1);
+            if constexpr (!kOther) st.start(c + 1);
             lc.fetch(vp + (t + kDeltaChunk) * p.sv.t, p.sv.t, rows - kDeltaChunk, g, col, mine);
         }
         const uint16_t *kt = st.k_tile(c), *qt = st.q_tile(c), *tt = st.first(c), *pt = st.second(c);
@@ -302,7 +320,8 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 #pragma unroll
                 for (int n = 0; n < NI; ++n) {
                     ka[b & 1][m].t[n] = read_row<NCH>(kt + n * kTile, 16 * m + r, 4 * b + g);
-                    qa[b & 1][m].t[n] = read_row<NCH>(qt + n * kTile, 16 * m + r, 4 * b + g);
+                    if constexpr (!kEnd && !kOther)
+                        qa[b & 1][m].t[n] = read_row<NCH>(qt + n * kTile, 16 * m + r, 4 * b + g);
                 }
         };
         auto read_tri = [&](const uint16_t *from, Frag<NS> *to) {
@@ -312,6 +331,17 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 for (int n = 0; n < NS; ++n)
                     to[i].t[n] = *reinterpret_cast<const bf16x8 *>(from + ((i * NS + n) * 64 + l) * 8);
         };
+        if constexpr (kOther) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                read_kq(b);
+                const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) qs[m] = mma<NI, NS>(ka[b & 1][m], sb, qs[m]);
+            }
+            st.store_other(c);
+            if (c + 1 < chunks) st.start(c + 1);
+        }
         read_kq(0);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
@@ -324,12 +354,12 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 ks[m] = mma<NI, NS>(ka[b & 1][m], sb, ks[m]);
-                qs[m] = mma<NI, NS>(qa[b & 1][m], sb, qs[m]);
+                if constexpr (!kEnd && !kOther) qs[m] = mma<NI, NS>(qa[b & 1][m], sb, qs[m]);
             }
             fence();
         }
         // X = beta V - beta e^G K S;  U = X + (T - 1) X
-        read_tri(pt, pf);
+        if constexpr (!kEnd) read_tri(pt, pf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
@@ -362,7 +392,7 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                                                               32 * b + 8 * (r & 3) + 4 * o);
         };
         read_kc(0);
-        {
+        if constexpr (!kEnd) {
             const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
             if constexpr (kKeep)
                 if (kept) {
@@ -411,7 +441,33 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             }
         }
     }
-    if (p.hL && mine) {
+    if constexpr (kEnd) {
+        if (unit) {  // row-major terms, as the composition reads them
+            uint16_t *out = p.ws.M + slot * 3 * KD * KD + col;
+            if (col < KD) {
+#pragma unroll
+                for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+                        float x = S[m][e], y = S[m][e + 1];
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) {
+                            const uint32_t w = split_pair(x, y);
+                            out[(n * KD + row) * KD] = uint16_t(w);
+                            out[(n * KD + row + 1) * KD] = uint16_t(w >> 16);
+                        }
+                    }
+            }
+        } else if (kept) {
+            float *out = p.ws.N + slot * p.ws.state + col;
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    out[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+        }
+    } else if (p.hL && mine && seg.last) {
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m)
 #pragma unroll
@@ -419,6 +475,76 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
                 if (row < p.K) p.hL[state_at + (long long)row * p.V] = S[m][e];
             }
+    }
+}
+
+// ------------------------------------------------------------ the split's composition
+// entry_{s+1} = M_s entry_s + N_s over one sequence's segments, in place of
+// N_s.  entry_1 is N_0.  A wave holds 16 columns, as in the recurrence; M's
+// terms are staged in LDS for the workgroup's four waves.
+template <typename T, int KD>
+__global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
+{
+    constexpr int NS = Terms<T, KD>::kSum, NCH = KD / 8, KB = KD / 32, kTile = KD * KD;
+    constexpr int kPlanes = KD > 128 ? 1 : NS;  // of M in LDS at a time
+    __shared__ __align__(16) uint16_t lds[kPlanes * kTile];
+    const int head = int(blockIdx.y), tid = int(threadIdx.x), l = tid & 63, r = l & 15, g = l >> 4;
+    const int col = int(blockIdx.x) * 64 + 16 * (tid >> 6) + r;  // below Vp: a multiple of 64
+    const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
+    const int per = (p.seqlen + kDeltaChunk - 1) / kDeltaChunk, L = p.ws.seg_chunks;
+    const int chunks = (seq.len + kDeltaChunk - 1) / kDeltaChunk, segs = (chunks + L - 1) / L;
+    const long long z0 = p.cu ? seq.chunk0 / L + int(blockIdx.z) : (long long)blockIdx.z * ((per + L - 1) / L);
+
+    f32x4 S[KD / 16], N[KD / 16];
+    auto load = [&](long long slot, f32x4 *to) {
+        const float *n = p.ws.N + slot * p.ws.state + col;
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[m][e] = n[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp];
+    };
+    if (segs > 1) load(z0 * p.h + head, S);
+    for (int s = 1; s + 1 < segs; ++s) {
+        const long long slot = (z0 + s) * p.h + head;
+        load(slot, N);
+        Frag<NS> sb[KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) sb[b] = split8<NS>(S[2 * b], S[2 * b + 1]);
+#pragma unroll
+        for (int first = 0; first < NS; first += kPlanes) {
+            __syncthreads();  // the last reads are done
+            const u32x4 *M = reinterpret_cast<const u32x4 *>(p.ws.M + slot * 3 * kTile + first * kTile);
+            for (int at = tid; at < kPlanes * kTile / 8; at += 256) {
+                const int n = at / (kTile / 8), t = at % (kTile / 8) / NCH, c = at % NCH;
+                *reinterpret_cast<u32x4 *>(lds + n * kTile + chunk_at<NCH>(t, c)) = M[at];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m) {
+                const int row = 32 * (m / 2) + 8 * (r >> 2) + 4 * (m % 2) + (r & 3);
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    if constexpr (kPlanes == NS) {
+                        Frag<NS> a;
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) a.t[n] = read_row<NCH>(lds + n * kTile, row, 4 * b + g);
+                        N[m] = mma<NS, NS>(a, sb[b], N[m]);
+                    } else {  // one term of M with the terms of S that it keeps
+                        const bf16x8 a = read_row<NCH>(lds, row, 4 * b + g);
+#pragma unroll
+                        for (int n = 0; n + first < NS; ++n) N[m] = mfma16(a, sb[b].t[n], N[m]);
+                    }
+                }
+            }
+        }
+        float *out = p.ws.N + slot * p.ws.state + col;
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m) {
+            S[m] = N[m];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+        }
     }
 }
 
@@ -439,12 +565,20 @@ hipError_t prep_kd(const DeltaArgs &a, const PrepParams &p, bool both, bool fast
 template <typename T, int KD, int kWaves, bool kFast>
 hipError_t scan_waves(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
 {
-    const dim3 grid((a.V + 16 * kWaves - 1) / (16 * kWaves), a.h, a.nseq), block(64 * kWaves);
+    const DeltaSplit split = delta_split(a.batch, a.seqlen, a.h, a.V, a.cu ? a.nseq : 0);
+    const int tiles = (a.V + 16 * kWaves - 1) / (16 * kWaves);
+    const dim3 grid(tiles, a.h, split.segs ? split.segs : a.nseq), block(64 * kWaves);
     if (log_enabled())
-        log_line("delta_fwd: delta_scan_kernel<in %s, K %d, waves %d, keep %d, fast %d>, grid (%u, %u, %u) x %u threads",
-                 type_tag<T>(), KD, kWaves, int(p.ws.S0 != nullptr), int(kFast), grid.x, grid.y, grid.z, block.x);
-    if (p.ws.S0) delta_scan_kernel<T, KD, kWaves, true, kFast><<<grid, block, 0, stream>>>(p);
-    else delta_scan_kernel<T, KD, kWaves, false, kFast><<<grid, block, 0, stream>>>(p);
+        log_line("delta_fwd: delta_scan_kernel<in %s, K %d, waves %d, keep %d, fast %d>, grid (%u, %u, %u) x %u threads, "
+                 "%d chunks a segment", type_tag<T>(), KD, kWaves, int(p.ws.S0 != nullptr), int(kFast), grid.x, grid.y,
+                 grid.z, block.x, split.seg_chunks);
+    if (split.segs) {
+        const dim3 ends(tiles + (KD + 16 * kWaves - 1) / (16 * kWaves), a.h, split.segs), compose(p.Vp / 64, a.h, a.nseq);
+        delta_scan_kernel<T, KD, kWaves, kEndRun, kFast><<<ends, block, 0, stream>>>(p);
+        delta_compose_kernel<T, KD><<<compose, dim3(256), 0, stream>>>(p);
+    }
+    if (p.ws.S0) delta_scan_kernel<T, KD, kWaves, kKeepRun, kFast><<<grid, block, 0, stream>>>(p);
+    else delta_scan_kernel<T, KD, kWaves, kPlainRun, kFast><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
 }
 
@@ -473,7 +607,7 @@ hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaWs &ws, bool both, h
 hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaWs &ws, hipStream_t stream)
 {
     const int es = a.in_bf16 ? 2 : 4;
-    const ScanParams p{a.seqlen, a.h / a.hk, a.h, a.K, a.V, delta_vp(a.V), a.out_bf16, a.scale, a.cu, a.q, a.k,
+    const ScanParams p{a.seqlen, a.nseq, a.h / a.hk, a.h, a.K, a.V, delta_vp(a.V), a.out_bf16, a.scale, a.cu, a.q, a.k,
                        a.v, a.h0, a.y, a.hL, a.sq, a.sk, a.sv, a.sy, ws};
     // the columns of v and y need no 16-byte accesses, only 64 steps in one buffer
     constexpr long long most = (1ll << 31) / 64 / 4;
@@ -487,14 +621,13 @@ hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaWs &ws, hipStream_t 
 size_t delta_fwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, int V, int num_seqs)
 {
     size_t bytes = 0;
-    delta_ws(nullptr, delta_chunks(batch, seqlen, num_seqs) * h, K, V, false, &bytes);
+    delta_ws(nullptr, batch, seqlen, h, K, V, num_seqs, false, &bytes);
     return bytes;
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs &a, hipStream_t stream)
 {
-    const long long recs = delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0) * a.h;
-    const DeltaWs ws = delta_ws(a.workspace, recs, a.K, a.V, a.checkpoints, nullptr);
+    const DeltaWs ws = delta_ws(a, a.checkpoints);
     const hipError_t e = launch_delta_prep(a, ws, a.checkpoints, stream);
     return e == hipSuccess ? launch_delta_scan(a, ws, stream) : e;
 }

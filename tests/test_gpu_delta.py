@@ -94,9 +94,35 @@ CASES = [
 ]
 
 
+# sequences that the library cuts into segments (few heads, many chunks)
+SPLIT = [
+    (BF16, [2500], False, 1, 1, 128, 64, {}),
+    (F32, [1100], False, 1, 2, 64, 40, dict(decay="none")),
+    (F32, [1601], False, 1, 1, 100, 130, dict(decay="reset")),
+    (BF16, [1500, 1500], False, 1, 2, 40, 200, dict(state=False)),
+    (BF16, [1090], False, 1, 1, 256, 20, {}),
+    (F32, [1153], False, 1, 1, 200, 10, {}),
+    (BF16, [700, 0, 1, 1500, 64, 900], True, 1, 2, 64, 48, {}),
+    (F32, [1024, 1025], True, 1, 1, 32, 16, dict(state=False, decay="strong")),
+]
+
+
 def name(c):
     return "%s-L%s%s-h%d.%d-K%d-V%d-%s" % (str(c[0])[6:], ".".join(map(str, c[1])), "p" if c[2] else "", c[3], c[4], c[5],
                                            c[6], "-".join(str(v) for v in c[7].values()))
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=name)
+def test_split_sequences(case):
+    dtype, lens, packed, hk, h, K, V, opt = case
+    need = ssm.lib().ssm_delta_fwd_workspace_bytes
+    size = (1 if packed else len(lens), sum(lens) if packed else lens[0], hk, h, K, V, len(lens) if packed else 0)
+    # the split's planes are in the workspace: more than the chunks' share of a long batch's
+    chunks = lambda b, L, n: (L + 63) // 64 + n if n else b * ((L + 63) // 64)  # noqa: E731
+    wide = (512, 640, hk, h, K, V, 0)
+    per = need(*wide) / chunks(512, 640, 0)
+    assert need(*size) > 1.01 * per * chunks(size[0], size[1], size[6])
+    test_forward_and_gradients(case)
 
 
 @pytest.mark.parametrize("case", CASES, ids=name)
