@@ -139,8 +139,10 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
             if (kept) record_store<NS, KB>(p.ws.dS1 + rec * NS * p.ws.state, col_tile, b, sb);
             fence();
+            for_terms<NI, NS>([&](int i, int j) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) U[m] = mma<NI, NS>(ka[b & 1][m], sb, U[m]);
+                for (int m = 0; m < 4; ++m) U[m] = mfma16(ka[b & 1][m].t[i], sb.t[j], U[m]);
+            });
             fence();
         }
         read_tri(tt, tf);
@@ -153,10 +155,12 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
             }
             fence();
+            for_terms<NS, NG>([&](int i, int j) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+                for (int b = 1; b >= 0; --b)
 #pragma unroll
-                for (int b = m / 2; b < 2; ++b) U[m] = mma<NS, NG>(pf[tri_upper(m, b)], yb[b], U[m]);
+                    for (int m = 0; m < 2 + 2 * b; ++m) U[m] = mfma16(pf[tri_upper(m, b)].t[i], yb[b].t[j], U[m]);
+            });
             fence();
         }
         // dX = dU + (T - 1)^T dU
@@ -180,11 +184,13 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
             fence();
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                X[m] = U[m];
+            for (int m = 0; m < 4; ++m) X[m] = U[m];
+            for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
-                for (int b = m / 2; b < 2; ++b) X[m] = mma<NS, NS>(tf[tri_upper(m, b)], ub[b], X[m]);
-            }
+                for (int b = 1; b >= 0; --b)
+#pragma unroll
+                    for (int m = 0; m < 2 + 2 * b; ++m) X[m] = mfma16(tf[tri_upper(m, b)].t[i], ub[b].t[j], X[m]);
+            });
             fence();
         }
         {
@@ -221,16 +227,20 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 if (b + 1 < KB) read_qk(b + 1);
                 fence();
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    f32x4 &d = S[2 * b + o];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] *= ec;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (!kOther) d = mma<NI, NS>(qc[b & 1][o][i], yb[i], d);
-                        d = mma<NI, NS>(kc[b & 1][o][i], xb[i], d);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    S[2 * b][e] *= ec;
+                    S[2 * b + 1][e] *= ec;
                 }
+                for_terms<NI, NS>([&](int i, int j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            f32x4 &d = S[2 * b + o];
+                            if constexpr (!kOther) d = mfma16(qc[b & 1][o][t].t[i], yb[t].t[j], d);
+                            d = mfma16(kc[b & 1][o][t].t[i], xb[t].t[j], d);
+                        }
+                });
             }
             if constexpr (kOther) {
                 st.store_other(c);
@@ -447,12 +457,15 @@ void delta_grad_kernel(const GradParams p)
                     dP[m] = mma<NG, NS>(yw, au[m & 1], dP[m]);
                     dM[m] = mma<NS, NS>(xw, au[m & 1], dM[m]);
                 }
+                for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
-                for (int n = 0; n < NTT; ++n) {
-                    ys[n][m] = mma<NG, NS>(ay[m & 1], sb[n], ys[n][m]);
-                    xs[n][m] = mma<NS, NS>(ax[m & 1], sb[n], xs[n][m]);
-                    us[n][m] = mma<NS, NS>(au[m & 1], db[n], us[n][m]);
-                }
+                    for (int n = 0; n < NTT; ++n) {
+                        if (i < NG)
+                            ys[n][m] = mfma16(ay[m & 1].t[i], sb[n].t[j], ys[n][m]);
+                        xs[n][m] = mfma16(ax[m & 1].t[i], sb[n].t[j], xs[n][m]);
+                        us[n][m] = mfma16(au[m & 1].t[i], db[n].t[j], us[n][m]);
+                    }
+                });
                 fence();
             }
         }

@@ -351,11 +351,13 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             if constexpr (kKeep)
                 if (kept) record_store<NS, KB>(p.ws.S0 + rec * NS * p.ws.state, col_tile, b, sb);
             fence();
+            for_terms<NI, NS>([&](int i, int j) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                ks[m] = mma<NI, NS>(ka[b & 1][m], sb, ks[m]);
-                if constexpr (!kEnd && !kOther) qs[m] = mma<NI, NS>(qa[b & 1][m], sb, qs[m]);
-            }
+                for (int m = 0; m < 4; ++m) {
+                    ks[m] = mfma16(ka[b & 1][m].t[i], sb.t[j], ks[m]);
+                    if constexpr (!kEnd && !kOther) qs[m] = mfma16(qa[b & 1][m].t[i], sb.t[j], qs[m]);
+                }
+            });
             fence();
         }
         // X = beta V - beta e^G K S;  U = X + (T - 1) X
@@ -372,11 +374,13 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
             fence();
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                U[m] = X[m];
+            for (int m = 0; m < 4; ++m) U[m] = X[m];
+            for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
-                for (int b = 0; b <= m / 2; ++b) U[m] = mma<NS, NS>(tf[tri_lower(m, b)], xb[b], U[m]);
-            }
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int m = 2 * b; m < 4; ++m) U[m] = mfma16(tf[tri_lower(m, b)].t[i], xb[b].t[j], U[m]);
+            });
             fence();
         }
         // Y = scale e^G Q S + P U
@@ -406,10 +410,12 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 for (int e = 0; e < 4; ++e) qs[m][e] *= p.scale * eg[e];
             }
             fence();
+            for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int b = 0; b <= m / 2; ++b) qs[m] = mma<NS, NS>(pf[tri_lower(m, b)], ub[b], qs[m]);
+                    for (int m = 2 * b; m < 4; ++m) qs[m] = mfma16(pf[tri_lower(m, b)].t[i], ub[b].t[j], qs[m]);
+            });
             fence();
             const long long at = y0 + t * p.sy.t;
             if (p.y && p.out_bf16)
@@ -432,12 +438,17 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                 if (b + 1 < KB) read_kc(b + 1);
                 fence();
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[2 * b + o][e] *= ec;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) S[2 * b + o] = mma<NI, NS>(kc[b & 1][o][i], wb[i], S[2 * b + o]);
+                for (int e = 0; e < 4; ++e) {
+                    S[2 * b][e] *= ec;
+                    S[2 * b + 1][e] *= ec;
                 }
+                for_terms<NI, NS>([&](int i, int j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o)
+                            S[2 * b + o] = mfma16(kc[b & 1][o][t].t[i], wb[t].t[j], S[2 * b + o]);
+                });
             }
         }
     }

@@ -39,18 +39,24 @@ template <int N> struct Frag {
     bf16x8 t[N];
 };
 
-// The largest product first: where it cancels what c holds (U = X + (T - 1) X
-// under keys that point the same way), the small ones are then added to what
-// is left and not rounded at the size of c.
-template <int NA, int NB>
-__device__ inline f32x4 mma(const Frag<NA> &a, const Frag<NB> &b, f32x4 c)
+// f(i, j) for the pairs of terms that a product keeps, the largest first: where
+// it cancels what the sum holds (U = X + (T - 1) X under keys that point the
+// same way), the small ones are then added to what is left and not rounded at
+// the size of the sum.  Several products' pairs are issued in turn, so that no
+// matrix instruction waits for the one before it.
+template <int NA, int NB, typename F> __device__ inline void for_terms(F &&f)
 {
     constexpr int kOrder = NA == 3 && NB == 3 ? 3 : (NA > NB ? NA : NB) - 1;
 #pragma unroll
     for (int o = 0; o <= kOrder; ++o)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (o - i >= 0 && o - i < NB) c = mfma16(a.t[i], b.t[o - i], c);
+            if (o - i >= 0 && o - i < NB) f(i, o - i);
+}
+template <int NA, int NB>
+__device__ inline f32x4 mma(const Frag<NA> &a, const Frag<NB> &b, f32x4 c)
+{
+    for_terms<NA, NB>([&](int i, int j) { c = mfma16(a.t[i], b.t[j], c); });
     return c;
 }
 

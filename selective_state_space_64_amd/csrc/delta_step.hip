@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void delta_steps_kernel(const StepParams 
         if (p.s0 && row < K) {
             const float *s = p.s0 + at + (long long)row * V + c0;
             if (kVec) {
-                if (c0 < V) S[i] = *reinterpret_cast<const f32x4 *>(s);
+                if (c0 < V) S[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(s));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kThreads) void delta_steps_kernel(const StepParams 
         if (row < K) {
             float *s = p.s1 + at + (long long)row * V + c0;
             if (kVec) {
-                if (c0 < V) *reinterpret_cast<f32x4 *>(s) = S[i];
+                if (c0 < V) __builtin_nontemporal_store(S[i], reinterpret_cast<f32x4 *>(s));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -206,18 +206,20 @@ hipError_t launch_cols(const StepParams &p, int nseq, bool vec, hipStream_t stre
     if (p.K <= down) return launch_rows<T, TOut, kCols, 1>(p, nseq, vec, stream);
     if (p.K <= 2 * down) return launch_rows<T, TOut, kCols, 2>(p, nseq, vec, stream);
     if (p.K <= 4 * down) return launch_rows<T, TOut, kCols, 4>(p, nseq, vec, stream);
-    if constexpr (down * 4 < kDeltaMaxK)
-        if (p.K <= 8 * down) return launch_rows<T, TOut, kCols, 8>(p, nseq, vec, stream);
-    if constexpr (down * 8 < kDeltaMaxK) return launch_rows<T, TOut, kCols, 16>(p, nseq, vec, stream);
+    if constexpr (down * 4 < kDeltaMaxK) return launch_rows<T, TOut, kCols, 8>(p, nseq, vec, stream);
     return hipErrorInvalidValue;
 }
 
 template <typename T, typename TOut>
 hipError_t launch_typed(const StepParams &p, int nseq, bool vec, hipStream_t stream)
 {
-    // narrow tiles where wide ones would leave compute units without work
-    const long long wide = (long long)((p.V + 63) / 64) * p.h * nseq;
-    return wide >= 1024 ? launch_cols<T, TOut, 64>(p, nseq, vec, stream)
+    // Tiles of 32 columns move the most bytes a second; 16 where those would
+    // leave compute units without work.  64 states of 40 heads of 128 x 128, out
+    // of memory: 16 columns 119 us, 32 67.5, 64 91, 128 69 (336 MB; a copy of as
+    // many bytes 69 us); 74 us with 32 columns and ordinary in place of
+    // nontemporal accesses.
+    const long long wide = (long long)((p.V + 31) / 32) * p.h * nseq;
+    return wide >= 1024 ? launch_cols<T, TOut, 32>(p, nseq, vec, stream)
                         : launch_cols<T, TOut, 16>(p, nseq, vec, stream);
 }
 

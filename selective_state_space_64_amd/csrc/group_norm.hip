@@ -387,24 +387,32 @@ __global__ __launch_bounds__(kWgThreads) void norm_wg_kernel(const NormParams p)
     }
 }
 
-// Sums of the partial rows, in their order: 16 runs of rows per channel, then
-// the 16 sums.
+// Sums of the partial rows, in a fixed order: 16 runs of rows per channel, four
+// sums a run (their loads do not wait for one another), then the 64 sums.
 __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *pw, const float *pb, int splits,
                                                          int dim, float *dweight, float *dbias)
 {
     __shared__ float part[16][64];
     const int c = blockIdx.x * 64 + int(threadIdx.x & 63), run = int(threadIdx.x >> 6);
-    const float *src = blockIdx.y ? pb : pw;
+    const float *src = (blockIdx.y ? pb : pw) + c;
     float *dst = blockIdx.y ? dbias : dweight;
     if (!dst) return;  // the whole workgroup
-    float s = 0.0f;
-    if (c < dim)
-        for (int i = run; i < splits; i += 16) s += src[(long long)i * dim + c];
-    part[run][threadIdx.x & 63] = s;
+    float s[4] = {0, 0, 0, 0};
+    if (c < dim) {
+        int i = run;
+        for (; i + 48 < splits; i += 64)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += src[(long long)(i + 16 * j) * dim];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 16 * j < splits) s[j] += src[(long long)(i + 16 * j) * dim];
+    }
+    part[run][threadIdx.x & 63] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     if (run == 0 && c < dim) {
-        for (int i = 1; i < 16; ++i) s += part[i][threadIdx.x];
-        dst[c] = s;
+        float t = part[0][threadIdx.x];
+        for (int i = 1; i < 16; ++i) t += part[i][threadIdx.x];
+        dst[c] = t;
     }
 }
 
