@@ -51,10 +51,10 @@ struct ScanBwdParams {
     DeltaWs ws;
 };
 
-template <typename T, typename TG, int KD, int kWaves, bool kFast>
+template <typename T, typename TG, int KD, int kWaves, int kPath>
 __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_bwd_kernel(const ScanBwdParams p)
 {
-    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>;
+    constexpr bool kFast = kPath >= kByRun, kAsync = kPath == kByCopy;
     using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, true, true>;
     constexpr int NI = Stage::NI, NS = Stage::NS, NG = kGradTerms<T, TG, KD>;
     constexpr int NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
@@ -75,6 +75,10 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h, p.sq.t,
             p.ws.prep + rec0 * p.ws.prep_stride, p.h * p.ws.prep_stride, seq.len, p.K);
     const TG *yp = static_cast<const TG *>(p.dy) + seq.batch * p.sdy.b + seq.first * p.sdy.t + head * p.sdy.h;
+    if constexpr (kAsync) {
+        const int first = int(blockIdx.x) * 16 * kWaves;
+        st.init_columns(yp + first, p.sdy.t, p.V - first);
+    }
     TG *vp = static_cast<TG *>(p.dv) + seq.batch * p.sdv.b + seq.first * p.sdv.t + head * p.sdv.h;
 
     // dS, laid out as S in the forward
@@ -92,7 +96,7 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
     auto fetch = [&](int c) {
         if (!kOther || c == chunks - 1) st.start(c);
         const long long t = (long long)c * kDeltaChunk;
-        lc.fetch(yp + t * p.sdy.t, p.sdy.t, seq.len - c * kDeltaChunk, g, col, mine);
+        if constexpr (!kAsync) lc.fetch(yp + t * p.sdy.t, p.sdy.t, seq.len - c * kDeltaChunk, g, col, mine);
     };
     if (chunks > 0) fetch(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
@@ -106,7 +110,10 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
         st.store(c);
         f32x4 Y[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) Y[m] = lc.tile(m, rows, g, mine);
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (kAsync) Y[m] = st.column(c, m);
+            else Y[m] = lc.tile(m, rows, g, mine);
+        }
         if (c > 0) fetch(c - 1);
         const uint16_t *kt = st.k_tile(c), *qt = st.q_tile(c), *tt = st.first(c), *pt = st.second(c);
         const float *vec = st.vec(c);
@@ -723,20 +730,24 @@ hipError_t launch_typed(const DeltaBwdArgs &b, const DeltaWs &ws, hipStream_t st
                            b.dh0, a.sq, a.sk, b.sdy, b.sdv, ws};
     const GradParams gp{a.seqlen, a.nseq, rep, a.h, a.K, a.V, Vp, a.scale, a.cu, a.q, a.k, a.v, b.dy, a.g, a.beta,
                         b.dq, b.dk, b.dg, b.dbeta, a.sq, a.sk, a.sv, a.sg, a.sbeta, b.sdy, b.sdq, b.sdk, ws};
-    const bool wide = kDeltaAsync<T, KD> && sfast && delta_wide(a);
-    const int waves = wide ? 8 : 4;
+    constexpr bool kCan = kDeltaAsync<T, KD> && sizeof(TG) == 2;
+    const int path = !sfast ? kByElement : kCan && delta_fast(b.dy, b.sdy, a.V, gs, a, a.h) ? kByCopy : kByRun;
+    const int waves = path == kByCopy && delta_wide(a) ? 8 : 4;
     const dim3 sgrid((a.V + 16 * waves - 1) / (16 * waves), a.h, a.nseq), sblock(64 * waves);
     const dim3 ggrid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.hk), gblock(kThreads);
     if (log_enabled())
-        log_line("delta_bwd: delta_scan_bwd_kernel, delta_grad_kernel<in %s, grad %s, K %d>, fast %d, %d, "
-                 "grids (%u, %u, %u) x %u, (%u, %u) x %u threads", type_tag<T>(), type_tag<TG>(), KD, int(sfast),
+        log_line("delta_bwd: delta_scan_bwd_kernel, delta_grad_kernel<in %s, grad %s, K %d>, paths %d, %d, "
+                 "grids (%u, %u, %u) x %u, (%u, %u) x %u threads", type_tag<T>(), type_tag<TG>(), KD, path,
                  int(gfast), sgrid.x, sgrid.y, sgrid.z, sblock.x, ggrid.x, ggrid.y, gblock.x);
-    if (!sfast) {
-        delta_scan_bwd_kernel<T, TG, KD, 4, false><<<sgrid, sblock, 0, stream>>>(sp);
-    } else if (!wide) {
-        delta_scan_bwd_kernel<T, TG, KD, 4, true><<<sgrid, sblock, 0, stream>>>(sp);
+    if (path == kByElement) {
+        delta_scan_bwd_kernel<T, TG, KD, 4, kByElement><<<sgrid, sblock, 0, stream>>>(sp);
+    } else if (path == kByRun) {
+        delta_scan_bwd_kernel<T, TG, KD, 4, kByRun><<<sgrid, sblock, 0, stream>>>(sp);
     } else {
-        if constexpr (kDeltaAsync<T, KD>) delta_scan_bwd_kernel<T, TG, KD, 8, true><<<sgrid, sblock, 0, stream>>>(sp);
+        if constexpr (kCan) {
+            if (waves == 8) delta_scan_bwd_kernel<T, TG, KD, 8, kByCopy><<<sgrid, sblock, 0, stream>>>(sp);
+            else delta_scan_bwd_kernel<T, TG, KD, 4, kByCopy><<<sgrid, sblock, 0, stream>>>(sp);
+        }
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -202,10 +202,14 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
     // then brings Q (kUpper: K), store_other() the other in its place
     static constexpr bool kOneTile = NI * KD > 512;
     static constexpr int kTiles = kOneTile ? 1 : 2;
-    static constexpr int kBuffers = kAsync ? 2 : 1, kBuffer = kTiles * NI * kTile + kPart;  // u16 elements
+    // kAsync: the workgroup's columns of V (or dY) too, 64 steps of kCols
+    static constexpr int kCols = 16 * kWaves, kColChunks = kCols / 8, kColTile = kAsync ? 64 * kCols : 0;
+    static constexpr int kColRows = kThreads / kColChunks;
+    static constexpr int kBuffers = kAsync ? 2 : 1, kBuffer = kTiles * NI * kTile + kPart + kColTile;  // u16 elements
     static constexpr int kPartLoads = (kPart / 8 + kThreads - 1) / kThreads;
     static constexpr int kRows = kThreads / NCH;  // rows of one copy of all threads
-    static_assert(!kAsync || (NI == 1 && kFast && kRows % 16 == 0), "rows as they are; the same chunk order in each copy");
+    static_assert(!kAsync || (NI == 1 && kFast && kRows % 16 == 0),
+                  "rows as they are; the same chunk order in each copy");
 
     uint16_t *lds;
     const T *kp, *qp;
@@ -214,7 +218,33 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
     int len, K;
     TileLoad<T, NCH, kThreads, kFast> lk, lq;
     u32x4 lt[kAsync ? 1 : kPartLoads];
-    uint32_t k_off, q_off;
+    uint32_t k_off, q_off, c_off;
+    const uint16_t *cp;
+    long long c_step;
+
+    // The columns from c0 on, n of them there (bf16; kAsync).
+    __device__ inline void init_columns(const void *c0, long long cst, int n)
+    {
+        const int t = int(threadIdx.x) / kColChunks;
+        const int c = (chunk_at<kColChunks>(t, int(threadIdx.x) % kColChunks) / 8) % kColChunks;
+        cp = static_cast<const uint16_t *>(c0);
+        c_step = cst;
+        c_off = c * 8 < n ? uint32_t(t * int(cst) + c * 8) * 2u : kOutside;
+    }
+    // The wave's 16 columns of them as D tile m: a lane's column, steps 16 m + 4 g + {0..3}
+    __device__ inline f32x4 column(int c, int m) const
+    {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const int l = int(threadIdx.x) & 63, r = l & 15, g = l >> 4;
+        const int col4 = 16 * (int(threadIdx.x) >> 6) + 4 * (r & 3);
+        const uint16_t *tile = buffer(c) + kTiles * NI * kTile + kPart;
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(tile + chunk_at<kColChunks>(16 * m + 4 * g + (r >> 2), col4 >> 3) + (col4 & 4)));
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(uint32_t(uint16_t(x[e])) << 16);
+        return v;
+    }
 
     // k0, q0: the sequence's first step; rec0: the record of its first chunk,
     // records of a head rec_step elements apart
@@ -267,6 +297,11 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
                                 to + kTile * 2 + i * kThreads * 16);
             }
             copy_linear<kWaves>(part, kPart * 2, lds_offset(buffer(c)) + 4 * kTile);
+            const uint16_t *col = cp + (long long)c * kDeltaChunk * c_step;
+#pragma unroll
+            for (int i = 0; i < 64 / kColRows; ++i)
+                copy_to_lds(copy_buffer(col + (long long)(i * kColRows) * c_step, (rows - i * kColRows) * c_step * 2), c_off,
+                            to + 4 * kTile + 2 * kPart + i * kThreads * 16);
         } else {
             lk.fetch(k, k_step, rows, K);
             if constexpr (kNeedQ) lq.fetch(q, q_step, rows, K);
@@ -305,8 +340,10 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
     }
 };
 
-// Whether a call's recurrence takes the asynchronous form, and whether with
-// eight waves a workgroup (128 columns) in place of four.
+// How a call's recurrence reads its rows: element by element, in 16-byte runs
+// through registers, or copied straight to LDS (bf16, two buffers: K <= 128),
+// and then whether with eight waves a workgroup (128 columns) in place of four.
+enum { kByElement = 0, kByRun = 1, kByCopy = 2 };
 template <typename T, int KD> constexpr bool kDeltaAsync = sizeof(T) == 2 && KD <= 128;
 inline bool delta_wide(const DeltaArgs &a) { return a.V > 64; }
 

@@ -74,16 +74,16 @@ __device__ inline void write_tri(const float *m, int diag, uint16_t *out)
 }
 
 template <typename T, int KD, bool kBoth, bool kFast>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p)
+__global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && kFast ? 4 : 1)) void delta_prep_kernel(const PrepParams p)
 {
     constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
     constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;
-    constexpr int kTiles = 2 * NI * kTile * 2, kMats = 3 * 64 * kPitch * 4;
+    constexpr int kTiles = 2 * NI * kTile * 2, kMats = 2 * 64 * kPitch * 4;
     __shared__ __align__(16) unsigned char lds[kTiles > kMats ? kTiles : kMats];
     __shared__ double G[64];
     __shared__ float beta[64];
     uint16_t *kt = reinterpret_cast<uint16_t *>(lds), *qt = kt + NI * kTile;
-    float *M = reinterpret_cast<float *>(lds), *P = M + 64 * kPitch, *Tm = P + 64 * kPitch;
+    float *M = reinterpret_cast<float *>(lds), *P = M + 64 * kPitch, *Tm = P;
 
     const int chunk = int(blockIdx.x), head = int(blockIdx.y);
     const int si = delta_seq_of(p.cu, p.nseq, p.seqlen, chunk);
@@ -165,18 +165,21 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
         }
     __syncthreads();
 
-    // T: the diagonal blocks by forward substitution, lane r one column (the
-    // four lane groups alike)
+    // P leaves, T takes its place.  T's diagonal blocks by forward substitution,
+    // lane r one column (the four lane groups alike); every finished entry is
+    // taken from those below it, which do not wait for one another.
+    write_tri<NS, false>(P, 0, out + tri_size(NS));
+    if constexpr (kBoth) write_tri<NS, true>(P, 0, out + 3 * tri_size(NS) + 512);
     {
         const float *m = M + (16 * wave) * kPitch + 16 * wave;
         float t[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = i == r ? 1.0f : 0.0f;
+        for (int i = 0; i < 16; ++i) t[i] = i == r ? 1.0f : 0.0f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) v = __builtin_fmaf(-m[i * kPitch + j], t[j], v);
-            t[i] = v;
-        }
+        for (int j = 0; j < 15; ++j)
+#pragma unroll
+            for (int i = j + 1; i < 16; ++i) t[i] = __builtin_fmaf(-m[i * kPitch + j], t[j], t[i]);
+        __syncthreads();  // P is read
         if (g == 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) Tm[(16 * wave + i) * kPitch + 16 * wave + r] = t[i];
@@ -207,11 +210,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const PrepParams p
         __syncthreads();
     }
     write_tri<NS, false>(Tm, 1, out);
-    write_tri<NS, false>(P, 0, out + tri_size(NS));
-    if constexpr (kBoth) {
-        write_tri<NS, true>(Tm, 1, out + 2 * tri_size(NS) + 512);
-        write_tri<NS, true>(P, 0, out + 3 * tri_size(NS) + 512);
-    }
+    if constexpr (kBoth) write_tri<NS, true>(Tm, 1, out + 2 * tri_size(NS) + 512);
 }
 
 // ------------------------------------------------------------ the recurrence
@@ -232,10 +231,10 @@ struct ScanParams {
 // chunk; or only a segment's end state and transfer matrix.
 enum { kPlainRun = 0, kKeepRun = 1, kEndRun = 2 };
 
-template <typename T, int KD, int kWaves, int kRun, bool kFast>
+template <typename T, int KD, int kWaves, int kRun, int kPath>
 __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan_kernel(const ScanParams p)
 {
-    constexpr bool kAsync = kFast && kDeltaAsync<T, KD>, kKeep = kRun == kKeepRun, kEnd = kRun == kEndRun;
+    constexpr bool kFast = kPath >= kByRun, kAsync = kPath == kByCopy, kKeep = kRun == kKeepRun, kEnd = kRun == kEndRun;
     using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, false, !kEnd>;
     constexpr int NI = Stage::NI, NS = Stage::NS, NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
     constexpr int kKept = kKeep ? (KB + 2) * NS : 0;  // stores of a chunk beside y's 16
@@ -264,6 +263,10 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             static_cast<const T *>(p.q) + seq.batch * p.sq.b + seq.first * p.sq.t + (head / p.rep) * p.sq.h, p.sq.t,
             p.ws.prep + rec0 * p.ws.prep_stride, p.h * p.ws.prep_stride, seq.len, p.K);
     const T *vp = static_cast<const T *>(p.v) + seq.batch * p.sv.b + seq.first * p.sv.t + head * p.sv.h;
+    if constexpr (kAsync) {
+        const int first = int(blockIdx.x) * 16 * kWaves;
+        st.init_columns(vp + first, p.sv.t, unit ? 0 : p.V - first);
+    }
     const long long y0 = seq.batch * p.sy.b + seq.first * p.sy.t + head * p.sy.h;
 
     // S: tiles 2 b and 2 b + 1 hold the rows 32 b + 8 g + {0..3} and + {4..7}
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
     if (chunks > c0) {
         const long long t = (long long)c0 * kDeltaChunk;
         st.start(c0);
-        lc.fetch(vp + t * p.sv.t, p.sv.t, seq.len - c0 * kDeltaChunk, g, col, mine);
+        if constexpr (!kAsync) lc.fetch(vp + t * p.sv.t, p.sv.t, seq.len - c0 * kDeltaChunk, g, col, mine);
     }
     for (int c = c0; c < chunks; ++c) {
         const int rows = seq.len - c * kDeltaChunk;
@@ -298,11 +301,15 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
         st.store(c);
         f32x4 X[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) X[m] = lc.tile(m, rows, g, mine);
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (kAsync) X[m] = st.column(c, m);
+            else X[m] = lc.tile(m, rows, g, mine);
+        }
         constexpr bool kOther = Stage::kOneTile && !kEnd;  // K takes Q's place after Q S
         if (c + 1 < chunks) {
             if constexpr (!kOther) st.start(c + 1);
-            lc.fetch(vp + (t + kDeltaChunk) * p.sv.t, p.sv.t, rows - kDeltaChunk, g, col, mine);
+            if constexpr (!kAsync)
+                lc.fetch(vp + (t + kDeltaChunk) * p.sv.t, p.sv.t, rows - kDeltaChunk, g, col, mine);
         }
         const uint16_t *kt = st.k_tile(c), *qt = st.q_tile(c), *tt = st.first(c), *pt = st.second(c);
         const float *vec = st.vec(c);
@@ -343,25 +350,28 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             if (c + 1 < chunks) st.start(c + 1);
         }
         read_kq(0);
+        Frag<NS> sb[2];
+        sb[0] = split8<NS>(S[0], S[1]);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
-            if (b + 1 < KB) read_kq(b + 1);
-            else read_tri(tt, tf);
-            const Frag<NS> sb = split8<NS>(S[2 * b], S[2 * b + 1]);
+            if (b + 1 < KB) {
+                read_kq(b + 1);
+                sb[(b + 1) & 1] = split8<NS>(S[2 * b + 2], S[2 * b + 3]);
+            } else {
+                read_tri(tt, tf);
+            }
             if constexpr (kKeep)
-                if (kept) record_store<NS, KB>(p.ws.S0 + rec * NS * p.ws.state, col_tile, b, sb);
-            fence();
+                if (kept) record_store<NS, KB>(p.ws.S0 + rec * NS * p.ws.state, col_tile, b, sb[b & 1]);
             for_terms<NI, NS>([&](int i, int j) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    ks[m] = mfma16(ka[b & 1][m].t[i], sb.t[j], ks[m]);
-                    if constexpr (!kEnd && !kOther) qs[m] = mfma16(qa[b & 1][m].t[i], sb.t[j], qs[m]);
+                    ks[m] = mfma16(ka[b & 1][m].t[i], sb[b & 1].t[j], ks[m]);
+                    if constexpr (!kEnd && !kOther) qs[m] = mfma16(qa[b & 1][m].t[i], sb[b & 1].t[j], qs[m]);
                 }
             });
-            fence();
+            interleave<(kEnd || kOther ? 4 : 8) * NI, 8 * NS, 3>();
         }
         // X = beta V - beta e^G K S;  U = X + (T - 1) X
-        if constexpr (!kEnd) read_tri(pt, pf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * m + 4 * g);
@@ -370,9 +380,11 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             for (int e = 0; e < 4; ++e) X[m][e] = __builtin_fmaf(bt[e], X[m][e], -be[e] * ks[m][e]);
         }
         f32x4 U[4];
+        const float ec = vec[63];
         {
             const Frag<NS> xb[2] = {split8<NS>(X[0], X[1]), split8<NS>(X[2], X[3])};
             fence();
+            if constexpr (!kEnd) read_tri(pt, pf);
 #pragma unroll
             for (int m = 0; m < 4; ++m) U[m] = X[m];
             for_terms<NS, NS>([&](int i, int j) {
@@ -381,9 +393,22 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 #pragma unroll
                     for (int m = 2 * b; m < 4; ++m) U[m] = mfma16(tf[tri_lower(m, b)].t[i], xb[b].t[j], U[m]);
             });
-            fence();
+            // beside them: Q S and S take their decays
+            if constexpr (!kEnd) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qs[m][e] *= p.scale * eg[e];
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][e] *= ec;
+            interleave<(kEnd ? 0 : 6 * NS + 4), 18, 3>();
         }
-        // Y = scale e^G Q S + P U
+        // Y = scale e^G Q S + P U;  beside it e^{Gc - G} U
         Frag<NI> kc[2][2][2];  // K^T: [step parity][tile of the pair][time block]
         auto read_kc = [&](int b) {
 #pragma unroll
@@ -395,7 +420,17 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                         kc[b & 1][o][i].t[n] = read_cols<NCH>(kt + n * kTile, 32 * i + 4 * g, 32 * i + 16 + 4 * g,
                                                               32 * b + 8 * (r & 3) + 4 * o);
         };
-        read_kc(0);
+        Frag<NS> wb[2];
+        auto tailed = [&]() {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
+            }
+            wb[0] = split8<NS>(U[0], U[1]);
+            wb[1] = split8<NS>(U[2], U[3]);
+        };
         if constexpr (!kEnd) {
             const Frag<NS> ub[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
             if constexpr (kKeep)
@@ -403,53 +438,39 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
                     record_store<NS, 2>(p.ws.U + rec * NS * p.ws.step, col_tile, 0, ub[0]);
                     record_store<NS, 2>(p.ws.U + rec * NS * p.ws.step, col_tile, 1, ub[1]);
                 }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4 eg = *reinterpret_cast<const f32x4 *>(vec + 16 * m + 4 * g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qs[m][e] *= p.scale * eg[e];
-            }
             fence();
+            read_kc(0);
             for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int m = 2 * b; m < 4; ++m) qs[m] = mfma16(pf[tri_lower(m, b)].t[i], ub[b].t[j], qs[m]);
             });
+            tailed();
+            interleave<8 * NI + 4, 18, 4>();
             fence();
+        } else {
+            read_kc(0);
+            tailed();
+        }
+        // S = e^{Gc} S + K^T (e^{Gc - G} U);  beside it the stores of Y
+        if constexpr (!kEnd) {
             const long long at = y0 + t * p.sy.t;
             if (p.y && p.out_bf16)
                 store_column<bf16_t, kFast>(static_cast<bf16_t *>(p.y) + at, p.sy.t, rows, g, col, mine, qs);
             else if (p.y)
                 store_column<float, kFast>(static_cast<float *>(p.y) + at, p.sy.t, rows, g, col, mine, qs);
         }
-        // S = e^{Gc} S + K^T (e^{Gc - G} U)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4 tail = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * m + 4 * g);
+        for (int b = 0; b < KB; ++b) {
+            if (b + 1 < KB) read_kc(b + 1);
+            for_terms<NI, NS>([&](int i, int j) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) U[m][e] *= tail[e];
-        }
-        {
-            const Frag<NS> wb[2] = {split8<NS>(U[0], U[1]), split8<NS>(U[2], U[3])};
-            const float ec = vec[63];
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                if (b + 1 < KB) read_kc(b + 1);
-                fence();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[2 * b][e] *= ec;
-                    S[2 * b + 1][e] *= ec;
-                }
-                for_terms<NI, NS>([&](int i, int j) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int o = 0; o < 2; ++o)
-                            S[2 * b + o] = mfma16(kc[b & 1][o][t].t[i], wb[t].t[j], S[2 * b + o]);
-                });
-            }
+                    for (int o = 0; o < 2; ++o) S[2 * b + o] = mfma16(kc[b & 1][o][t].t[i], wb[t].t[j], S[2 * b + o]);
+            });
+            interleave<8 * NI, 4 * NS, 0>();
         }
     }
     if constexpr (kEnd) {
@@ -492,13 +513,15 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 // ------------------------------------------------------------ the split's composition
 // entry_{s+1} = M_s entry_s + N_s over one sequence's segments, in place of
 // N_s.  entry_1 is N_0.  A wave holds 16 columns, as in the recurrence; M's
-// terms are staged in LDS for the workgroup's four waves.
+// terms come to LDS for the workgroup's four waves, a segment ahead where two
+// of them fit.
 template <typename T, int KD>
 __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
 {
     constexpr int NS = Terms<T, KD>::kSum, NCH = KD / 8, KB = KD / 32, kTile = KD * KD;
     constexpr int kPlanes = KD > 128 ? 1 : NS;  // of M in LDS at a time
-    __shared__ __align__(16) uint16_t lds[kPlanes * kTile];
+    constexpr int kBuffers = 2 * kPlanes * kTile * 2 <= 160 * 1024 ? 2 : 1;
+    __shared__ __align__(16) uint16_t lds[kBuffers * kPlanes * kTile];
     const int head = int(blockIdx.y), tid = int(threadIdx.x), l = tid & 63, r = l & 15, g = l >> 4;
     const int col = int(blockIdx.x) * 64 + 16 * (tid >> 6) + r;  // below Vp: a multiple of 64
     const DeltaSeq seq = delta_seq(p.cu, int(blockIdx.z), p.seqlen);
@@ -507,30 +530,47 @@ __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
     const long long z0 = p.cu ? seq.chunk0 / L + int(blockIdx.z) : (long long)blockIdx.z * ((per + L - 1) / L);
 
     f32x4 S[KD / 16], N[KD / 16];
-    auto load = [&](long long slot, f32x4 *to) {
-        const float *n = p.ws.N + slot * p.ws.state + col;
+    auto load = [&](int s, f32x4 *to) {
+        const float *n = p.ws.N + ((z0 + s) * p.h + head) * p.ws.state + col;
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 to[m][e] = n[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp];
     };
-    if (segs > 1) load(z0 * p.h + head, S);
+    // terms [first, first + kPlanes) of M_s, rows' chunks in the tiles' order
+    constexpr int kRows = 256 / NCH;
+    uint32_t off[2];  // of even and odd runs of rows: their order differs where a run has 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        off[i] = uint32_t(tid / NCH * NCH + (chunk_at<NCH>(tid / NCH + i * kRows, tid % NCH) / 8) % NCH) * 16;
+    auto copy = [&](int s, int first) {
+        const uint16_t *M = p.ws.M + ((z0 + s) * p.h + head) * 3 * kTile + first * kTile;
+        const uint32_t to = lds_offset(lds + (kBuffers == 2 ? (s & 1) * kPlanes * kTile : 0)) + (tid >> 6) * 1024;
+        const sgpr4 buf = copy_buffer(M, kPlanes * kTile * 2);
+        for (int i = 0; i < kPlanes * KD / kRows; i += 2) {
+            copy_to_lds(buf, off[0] + i * 4096, to + i * 4096);
+            copy_to_lds(buf, off[1] + (i + 1) * 4096, to + (i + 1) * 4096);
+        }
+    };
+    static_assert(2 * kRows % 16 == 0 && KD / kRows % 2 == 0, "the same order in every second run");
+    if (segs > 1) load(0, S);
+    if (kBuffers == 2 && segs > 2) copy(1, 0);
     for (int s = 1; s + 1 < segs; ++s) {
-        const long long slot = (z0 + s) * p.h + head;
-        load(slot, N);
+        load(s, N);
+        const uint16_t *tile = lds + (kBuffers == 2 ? (s & 1) * kPlanes * kTile : 0);
         Frag<NS> sb[KB];
 #pragma unroll
         for (int b = 0; b < KB; ++b) sb[b] = split8<NS>(S[2 * b], S[2 * b + 1]);
 #pragma unroll
         for (int first = 0; first < NS; first += kPlanes) {
-            __syncthreads();  // the last reads are done
-            const u32x4 *M = reinterpret_cast<const u32x4 *>(p.ws.M + slot * 3 * kTile + first * kTile);
-            for (int at = tid; at < kPlanes * kTile / 8; at += 256) {
-                const int n = at / (kTile / 8), t = at % (kTile / 8) / NCH, c = at % NCH;
-                *reinterpret_cast<u32x4 *>(lds + n * kTile + chunk_at<NCH>(t, c)) = M[at];
+            if constexpr (kBuffers == 1) {
+                __syncthreads();  // the last reads are done
+                copy(s, first);
             }
+            wait_loads<0>();
             __syncthreads();
+            if (kBuffers == 2 && s + 2 < segs) copy(s + 1, 0);
 #pragma unroll
             for (int m = 0; m < KD / 16; ++m) {
                 const int row = 32 * (m / 2) + 8 * (r >> 2) + 4 * (m % 2) + (r & 3);
@@ -539,17 +579,17 @@ __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
                     if constexpr (kPlanes == NS) {
                         Frag<NS> a;
 #pragma unroll
-                        for (int n = 0; n < NS; ++n) a.t[n] = read_row<NCH>(lds + n * kTile, row, 4 * b + g);
+                        for (int n = 0; n < NS; ++n) a.t[n] = read_row<NCH>(tile + n * kTile, row, 4 * b + g);
                         N[m] = mma<NS, NS>(a, sb[b], N[m]);
                     } else {  // one term of M with the terms of S that it keeps
-                        const bf16x8 a = read_row<NCH>(lds, row, 4 * b + g);
+                        const bf16x8 a = read_row<NCH>(tile, row, 4 * b + g);
 #pragma unroll
                         for (int n = 0; n + first < NS; ++n) N[m] = mfma16(a, sb[b].t[n], N[m]);
                     }
                 }
             }
         }
-        float *out = p.ws.N + slot * p.ws.state + col;
+        float *out = p.ws.N + ((z0 + s) * p.h + head) * p.ws.state + col;
 #pragma unroll
         for (int m = 0; m < KD / 16; ++m) {
             S[m] = N[m];
@@ -573,33 +613,35 @@ hipError_t prep_kd(const DeltaArgs &a, const PrepParams &p, bool both, bool fast
     return hipGetLastError();
 }
 
-template <typename T, int KD, int kWaves, bool kFast>
+template <typename T, int KD, int kWaves, int kPath>
 hipError_t scan_waves(const DeltaArgs &a, const ScanParams &p, hipStream_t stream)
 {
     const DeltaSplit split = delta_split(a.batch, a.seqlen, a.h, a.V, a.cu ? a.nseq : 0);
     const int tiles = (a.V + 16 * kWaves - 1) / (16 * kWaves);
     const dim3 grid(tiles, a.h, split.segs ? split.segs : a.nseq), block(64 * kWaves);
     if (log_enabled())
-        log_line("delta_fwd: delta_scan_kernel<in %s, K %d, waves %d, keep %d, fast %d>, grid (%u, %u, %u) x %u threads, "
-                 "%d chunks a segment", type_tag<T>(), KD, kWaves, int(p.ws.S0 != nullptr), int(kFast), grid.x, grid.y,
+        log_line("delta_fwd: delta_scan_kernel<in %s, K %d, waves %d, keep %d, path %d>, grid (%u, %u, %u) x %u threads, "
+                 "%d chunks a segment", type_tag<T>(), KD, kWaves, int(p.ws.S0 != nullptr), kPath, grid.x, grid.y,
                  grid.z, block.x, split.seg_chunks);
     if (split.segs) {
         const dim3 ends(tiles + (KD + 16 * kWaves - 1) / (16 * kWaves), a.h, split.segs), compose(p.Vp / 64, a.h, a.nseq);
-        delta_scan_kernel<T, KD, kWaves, kEndRun, kFast><<<ends, block, 0, stream>>>(p);
+        delta_scan_kernel<T, KD, kWaves, kEndRun, kPath><<<ends, block, 0, stream>>>(p);
         delta_compose_kernel<T, KD><<<compose, dim3(256), 0, stream>>>(p);
     }
-    if (p.ws.S0) delta_scan_kernel<T, KD, kWaves, kKeepRun, kFast><<<grid, block, 0, stream>>>(p);
-    else delta_scan_kernel<T, KD, kWaves, kPlainRun, kFast><<<grid, block, 0, stream>>>(p);
+    if (p.ws.S0) delta_scan_kernel<T, KD, kWaves, kKeepRun, kPath><<<grid, block, 0, stream>>>(p);
+    else delta_scan_kernel<T, KD, kWaves, kPlainRun, kPath><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, int KD>
-hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, bool fast, hipStream_t stream)
+hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, int path, hipStream_t stream)
 {
-    if (!fast) return scan_waves<T, KD, 4, false>(a, p, stream);
-    if constexpr (kDeltaAsync<T, KD>)
-        if (delta_wide(a)) return scan_waves<T, KD, 8, true>(a, p, stream);
-    return scan_waves<T, KD, 4, true>(a, p, stream);
+    if (path == kByElement) return scan_waves<T, KD, 4, kByElement>(a, p, stream);
+    if constexpr (kDeltaAsync<T, KD>) {
+        if (path == kByCopy && delta_wide(a)) return scan_waves<T, KD, 8, kByCopy>(a, p, stream);
+        if (path == kByCopy) return scan_waves<T, KD, 4, kByCopy>(a, p, stream);
+    }
+    return scan_waves<T, KD, 4, kByRun>(a, p, stream);
 }
 
 }  // namespace
@@ -624,8 +666,9 @@ hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaWs &ws, hipStream_t 
     constexpr long long most = (1ll << 31) / 64 / 4;
     const bool fast = delta_fast(a.q, a.sq, a.K, es, a, a.hk) && delta_fast(a.k, a.sk, a.K, es, a, a.hk) &&
                       a.sv.t < most && a.sy.t < most;
+    const int path = !fast ? kByElement : delta_fast(a.v, a.sv, a.V, es, a, a.h) ? kByCopy : kByRun;
     return delta_dispatch(a.in_bf16, true, a.K, [&](auto t, auto, auto kd) {
-        return scan_kd<decltype(t), decltype(kd)::value>(a, p, fast, stream);
+        return scan_kd<decltype(t), decltype(kd)::value>(a, p, path, stream);
     });
 }
 

@@ -62,7 +62,5 @@ size_t delta_bwd_workspace_bytes(int batch, int seqlen, int hk, int h, int K, in
 hipError_t launch_delta_fwd(const DeltaArgs &a, hipStream_t stream);
 hipError_t launch_delta_bwd(const DeltaBwdArgs &a, hipStream_t stream);
 hipError_t launch_delta_update(const DeltaUpdateArgs &a, hipStream_t stream);
-// The recurrence step by step, for sequences of any length (delta_step.hip).
-hipError_t launch_delta_steps(const DeltaArgs &a, hipStream_t stream);
 
 }  // namespace ssm

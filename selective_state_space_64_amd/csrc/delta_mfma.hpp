@@ -92,6 +92,19 @@ template <int N> __device__ inline Frag<N> split8(f32x4 a, f32x4 b)
 // Keeps the instructions before it before those after it.
 __device__ inline void fence() { __builtin_amdgcn_sched_barrier(0); }
 
+// Orders what stands before it since the last fence: kReads LDS reads (of the
+// next phase) first, then kMatrix matrix instructions with kValu others behind
+// each.
+template <int kReads, int kMatrix, int kValu> __device__ inline void interleave()
+{
+    if constexpr (kReads > 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+#pragma unroll
+    for (int i = 0; i < kMatrix; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if constexpr (kValu > 0) __builtin_amdgcn_sched_group_barrier(0x2, kValu, 0);
+    }
+}
+
 // ---------------------------------------------------------------- LDS tiles
 // A tile of rows of NCH 16-byte chunks (8 bf16 each); a row's chunks are
 // permuted so that 16 rows' same chunk lie in different banks.
