@@ -414,10 +414,11 @@ void delta_grad_kernel(const GradParams p)
         for (int v0 = 0; v0 < p.V; v0 += 32) {
             if (v0) __syncthreads();  // the last columns' reads are done
             const long long tile = v0 / 16;
-            copy_linear<4>(S0 + tile * (kStates / 2), kStates * 2, lds_offset(ts));
-            copy_linear<4>(dS1 + tile * (kStates / 2), kStates * 2, lds_offset(td));
-            copy_linear<4>(U + tile * (kSteps / 2), kSteps * 2, lds_offset(tu));
-            copy_linear<4>(dX + tile * (kSteps / 2), kSteps * 2, lds_offset(tx));
+            const uint32_t to = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+            copy_linear<kStates * 2, 4>(S0 + tile * (kStates / 2), to, wave);
+            copy_linear<kStates * 2, 4>(dS1 + tile * (kStates / 2), to + 2 * kStates, wave);
+            copy_linear<kSteps * 2, 4>(U + tile * (kSteps / 2), to + 4 * kStates, wave);
+            copy_linear<kSteps * 2, 4>(dX + tile * (kSteps / 2), to + 4 * kStates + 2 * kSteps, wave);
             TileLoad<TG, 4, kThreads, kFast> ly;
             TileLoad<T, 4, kThreads, kFast> lv;
             ly.init(p.sdy.t, p.V - v0);

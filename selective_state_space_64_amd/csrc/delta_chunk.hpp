@@ -218,9 +218,10 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
     int len, K;
     TileLoad<T, NCH, kThreads, kFast> lk, lq;
     u32x4 lt[kAsync ? 1 : kPartLoads];
-    uint32_t k_off, q_off, c_off;
+    uint32_t k_off, q_off, c_off, lds0;  // lds0: the wave's place in the first buffer
     const uint16_t *cp;
     long long c_step;
+    int wave;
 
     // The columns from c0 on, n of them there (bf16; kAsync).
     __device__ inline void init_columns(const void *c0, long long cst, int n)
@@ -260,7 +261,9 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
         prep_step = rec_step;
         len = length;
         K = n;
+        wave = wave_of();
         if constexpr (kAsync) {
+            lds0 = __builtin_amdgcn_readfirstlane(lds_offset(buffers)) + wave * 1024;
             const int t = int(threadIdx.x) / NCH, c = (chunk_at<NCH>(t, int(threadIdx.x) % NCH) / 8) % NCH;
             k_off = c * 8 < n ? uint32_t(t * int(kst) + c * 8) * 2u : kOutside;
             q_off = c * 8 < n ? uint32_t(t * int(qst) + c * 8) * 2u : kOutside;
@@ -283,25 +286,23 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
     __device__ inline void start(int c)
     {
         const int rows = min(len - c * kDeltaChunk, kDeltaChunk);
-        const T *k = kp + (long long)c * kDeltaChunk * k_step, *q = qp + (long long)c * kDeltaChunk * q_step;
+        const T *k = kp + (long long)c * (kDeltaChunk * k_step), *q = qp + (long long)c * (kDeltaChunk * q_step);
         const uint16_t *part = prep + c * prep_step;
         if constexpr (kAsync) {
-            const uint32_t to = lds_offset(buffer(c)) + (threadIdx.x >> 6) * 1024;
+            // one buffer a tensor: 64 steps span less than 2^31 bytes
+            const uint32_t to = lds0 + (c & 1) * (kBuffer * 2);
+            const uint32_t kb = uint32_t(k_step) * 2, qb = uint32_t(q_step) * 2, cb = uint32_t(c_step) * 2;
+            const sgpr4 k_buf = copy_buffer(k, rows * kb), q_buf = copy_buffer(q, rows * qb);
+            const sgpr4 c_buf = copy_buffer(cp + (long long)c * (kDeltaChunk * c_step), rows * cb);
 #pragma unroll
             for (int i = 0; i < 64 / kRows; ++i) {
-                const int left = rows - i * kRows;
-                copy_to_lds(copy_buffer(k + (long long)(i * kRows) * k_step, left * k_step * 2), k_off,
-                            to + i * kThreads * 16);
-                if constexpr (kNeedQ)
-                    copy_to_lds(copy_buffer(q + (long long)(i * kRows) * q_step, left * q_step * 2), q_off,
-                                to + kTile * 2 + i * kThreads * 16);
+                copy_to_lds(k_buf, k_off + i * kRows * kb, to + i * kThreads * 16);
+                if constexpr (kNeedQ) copy_to_lds(q_buf, q_off + i * kRows * qb, to + kTile * 2 + i * kThreads * 16);
             }
-            copy_linear<kWaves>(part, kPart * 2, lds_offset(buffer(c)) + 4 * kTile);
-            const uint16_t *col = cp + (long long)c * kDeltaChunk * c_step;
+            copy_linear<kPart * 2, kWaves>(part, to - wave * 1024 + 4 * kTile, wave);
 #pragma unroll
             for (int i = 0; i < 64 / kColRows; ++i)
-                copy_to_lds(copy_buffer(col + (long long)(i * kColRows) * c_step, (rows - i * kColRows) * c_step * 2), c_off,
-                            to + 4 * kTile + 2 * kPart + i * kThreads * 16);
+                copy_to_lds(c_buf, c_off + i * kColRows * cb, to + 4 * kTile + 2 * kPart + i * kThreads * 16);
         } else {
             lk.fetch(k, k_step, rows, K);
             if constexpr (kNeedQ) lq.fetch(q, q_step, rows, K);

@@ -546,7 +546,8 @@ __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
         off[i] = uint32_t(tid / NCH * NCH + (chunk_at<NCH>(tid / NCH + i * kRows, tid % NCH) / 8) % NCH) * 16;
     auto copy = [&](int s, int first) {
         const uint16_t *M = p.ws.M + ((z0 + s) * p.h + head) * 3 * kTile + first * kTile;
-        const uint32_t to = lds_offset(lds + (kBuffers == 2 ? (s & 1) * kPlanes * kTile : 0)) + (tid >> 6) * 1024;
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds_offset(lds)) + wave_of() * 1024 +
+                            (kBuffers == 2 ? (s & 1) * kPlanes * kTile * 2 : 0);
         const sgpr4 buf = copy_buffer(M, kPlanes * kTile * 2);
         for (int i = 0; i < kPlanes * KD / kRows; i += 2) {
             copy_to_lds(buf, off[0] + i * 4096, to + i * 4096);

@@ -345,9 +345,9 @@ __device__ inline uint32_t lds_offset(const void *p)
 {
     return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
+// (lds: the same in every lane)
 __device__ inline void copy_to_lds(sgpr4 buf, uint32_t off, uint32_t lds)
 {
-    lds = __builtin_amdgcn_readfirstlane(lds);
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf) : "memory");
 }
 // Until at most N of the wave's vector-memory operations are under way (they
@@ -357,13 +357,17 @@ template <int N> __device__ inline void wait_loads()
     static_assert(N < 64, "the counter has 6 bits");
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// `bytes` (a multiple of 1 KB) of memory to LDS, spread over kWaves waves
-template <int kWaves> __device__ inline void copy_linear(const void *p, int bytes, uint32_t lds)
+__device__ inline int wave_of() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
+// kBytes (a multiple of 1 KB) of memory to LDS, spread over kWaves waves
+template <int kBytes, int kWaves> __device__ inline void copy_linear(const void *p, uint32_t lds, int wave)
 {
-    const sgpr4 buf = copy_buffer(p, bytes);
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    for (int at = wave * 1024; at < bytes; at += kWaves * 1024)
-        copy_to_lds(buf, uint32_t(at) + (threadIdx.x & 63) * 16, lds + at);
+    const sgpr4 buf = copy_buffer(p, kBytes);
+#pragma unroll
+    for (int i = 0; i < kBytes / 1024; i += kWaves) {
+        const int at = (i + wave) * 1024;
+        if (i + kWaves <= kBytes / 1024 || at < kBytes)
+            copy_to_lds(buf, uint32_t(i * 1024) + threadIdx.x * 16, lds + at);
+    }
 }
 
 // ---------------------------------------------------------------- records
