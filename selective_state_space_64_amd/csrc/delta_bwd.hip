@@ -733,7 +733,7 @@ hipError_t launch_typed(const DeltaBwdArgs &b, const DeltaWs &ws, hipStream_t st
                         b.dq, b.dk, b.dg, b.dbeta, a.sq, a.sk, a.sv, a.sg, a.sbeta, b.sdy, b.sdq, b.sdk, ws};
     constexpr bool kCan = kDeltaAsync<T, KD> && sizeof(TG) == 2;
     const int path = !sfast ? kByElement : kCan && delta_fast(b.dy, b.sdy, a.V, gs, a, a.h) ? kByCopy : kByRun;
-    const int waves = path == kByCopy && delta_wide(a) ? 8 : 4;
+    const int waves = path == kByCopy && delta_wide(a, false) ? 8 : 4;
     const dim3 sgrid((a.V + 16 * waves - 1) / (16 * waves), a.h, a.nseq), sblock(64 * waves);
     const dim3 ggrid(unsigned(delta_chunks(a.batch, a.seqlen, a.cu ? a.nseq : 0)), a.hk), gblock(kThreads);
     if (log_enabled())

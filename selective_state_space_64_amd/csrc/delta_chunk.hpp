@@ -21,15 +21,6 @@ template <typename T, int KD> struct Terms {
     static constexpr int kSum = sizeof(T) == 2 ? 2 : 3;
 };
 
-#ifndef DELTA_SPLIT_BELOW
-#define DELTA_SPLIT_BELOW 96
-#endif
-#ifndef DELTA_SPLIT_LEAST
-#define DELTA_SPLIT_LEAST 8
-#endif
-constexpr int kSplitBelow = DELTA_SPLIT_BELOW;  // workgroups of 128 columns
-constexpr int kSplitLeast = DELTA_SPLIT_LEAST;  // chunks
-
 struct DeltaWs {
     uint16_t *prep;     // prep_stride elements a record
     long long prep_stride;
@@ -49,8 +40,19 @@ struct DeltaWs {
 // segment but a sequence's last first yields its end state from zero (or h0)
 // and its K x K transfer matrix (the same recurrence on the unit columns, no
 // values), these are composed in order, and then all segments run at once.
-// That is about 2.2 times the work, over 256 / (heads x tiles) times the
-// workgroups.  Sizes only, so that the workspace is known before the call.
+// Sizes only, so that the workspace is known before the call.
+//
+// seg_chunks fills the card once (256 workgroups of 128 columns).  With few
+// heads that would be segments of one chunk, and composing s of them takes
+// s x 12 us of matrix products after one another, while a segment's two runs
+// take 2 x 4.2 us a chunk: about sqrt(chunks) segments are the least time.
+// Only sequences of more than four segments are split, the others lose more
+// to the second run and the two launches than they gain.  Measured, K = V =
+// 128, bf16, split against whole: 40 heads of 16384 steps 684 against 1025 us,
+// 8 heads of 4096 106 against 209, of 2048 78 against 112, 48 of 2048 134
+// against 133; below the rule 48 of 1024 90 against 73, 64 of 2048 152
+// against 137.  A packed batch is judged as if one sequence were all of it: the
+// sequences shorter than a segment cost no second run.
 struct DeltaSplit {
     int seg_chunks, segs;  // segs: an upper bound over all sequences
 };
@@ -58,13 +60,13 @@ inline DeltaSplit delta_split(int batch, int seqlen, int h, int V, int num_seqs)
 {
     const long long chunks = delta_chunks(batch, seqlen, num_seqs), nseq = num_seqs ? num_seqs : batch;
     const long long wgs = (long long)h * ((V + 127) / 128);
-    if (nseq * wgs > kSplitBelow) return {0, 0};
-    const long long want = 256 / wgs;  // segments in all
+    if (nseq * wgs > 256) return {0, 0};
+    const long long per = num_seqs ? chunks : chunks / batch;  // of the longest sequence
+    const long long want = 256 / wgs;                          // segments in all
     long long seg = (chunks + want - 1) / want;
-    if (seg < kSplitLeast) seg = kSplitLeast;
-    // no sequence of two segments (packed ones may all be short but one)
-    if (chunks < 2 * (num_seqs ? 1 : nseq) * seg) return {0, 0};
-    const long long per = (seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    if (seg < 4) seg = 4;
+    while ((seg + 1) * (seg + 1) <= per) ++seg;
+    if (per <= 4 * seg) return {0, 0};
     const long long segs = num_seqs ? chunks / seg + num_seqs : batch * ((per + seg - 1) / seg);
     return {int(seg), int(segs)};
 }
@@ -343,10 +345,17 @@ template <typename T, int KD, int kWaves, bool kFast, bool kAsync, bool kUpper, 
 
 // How a call's recurrence reads its rows: element by element, in 16-byte runs
 // through registers, or copied straight to LDS (bf16, two buffers: K <= 128),
-// and then whether with eight waves a workgroup (128 columns) in place of four.
+// and then with eight waves a workgroup (128 columns) or four.
 enum { kByElement = 0, kByRun = 1, kByCopy = 2 };
 template <typename T, int KD> constexpr bool kDeltaAsync = sizeof(T) == 2 && KD <= 128;
-inline bool delta_wide(const DeltaArgs &a) { return a.V > 64; }
+// Eight waves share a chunk's copies to LDS, which is what counts once every
+// compute unit has a workgroup (160 heads of 2048 steps: 217 us against 300);
+// four leave each wave more of a compute unit where twice the workgroups still
+// fit the card at one each (96 heads: 154 us against 181, 128: 179 against 200).
+inline bool delta_wide(const DeltaArgs &a, bool split)
+{
+    return a.V > 64 && (split || (long long)a.nseq * a.h * ((a.V + 127) / 128) > 128);
+}
 
 // Matrices of every chunk (delta_fwd.hip); both: the transposes too.
 hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaWs &ws, bool both, hipStream_t stream);

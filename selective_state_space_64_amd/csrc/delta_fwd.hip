@@ -639,7 +639,7 @@ hipError_t scan_kd(const DeltaArgs &a, const ScanParams &p, int path, hipStream_
 {
     if (path == kByElement) return scan_waves<T, KD, 4, kByElement>(a, p, stream);
     if constexpr (kDeltaAsync<T, KD>) {
-        if (path == kByCopy && delta_wide(a)) return scan_waves<T, KD, 8, kByCopy>(a, p, stream);
+        if (path == kByCopy && delta_wide(a, p.ws.seg_chunks)) return scan_waves<T, KD, 8, kByCopy>(a, p, stream);
         if (path == kByCopy) return scan_waves<T, KD, 4, kByCopy>(a, p, stream);
     }
     return scan_waves<T, KD, 4, kByRun>(a, p, stream);
