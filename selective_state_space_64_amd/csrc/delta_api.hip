@@ -71,8 +71,9 @@ Steps steps_of(const void *p, size_t span, size_t es, const ssm::DeltaStride &s,
                int batch)
 {
     const long long run = (heads - 1) * s.h + row;
-    if (seqlen == 1 || run > s.t) return {p, span * es, span * es, 0, 0};
-    return {p, span * es, size_t(run) * es, (long long)(s.t * es), batch == 1 ? 0 : (long long)(s.b * es)};
+    if (run > (seqlen == 1 ? s.b : s.t)) return {p, span * es, span * es, 0, 0};
+    return one_step({p, span * es, size_t(run) * es, (long long)(s.t * es),
+                                 batch == 1 ? 0 : (long long)(s.b * es)}, seqlen);
 }
 Steps range_of(const void *p, size_t bytes) { return {p, bytes, bytes, 0, 0}; }
 

@@ -555,7 +555,8 @@ ssm_status_t ssm_group_norm_fwd(int batch, int seqlen, int dim, int groups, ssm_
         const void *in = i ? z : x;
         const bool same = in == y && in_t == out_t && p.step[i] == p.step[3] && p.batch[i] == p.batch[3];
         const Steps a{in, sp[i] * es, dim * es, (long long)(p.step[i] * es), (long long)(p.batch[i] * es)};
-        if (!same && overlaps(a, Steps{y, ybytes, dim * os, (long long)(p.step[3] * os), (long long)(p.batch[3] * os)}))
+        const Steps to{y, ybytes, dim * os, (long long)(p.step[3] * os), (long long)(p.batch[3] * os)};
+        if (!same && overlaps(one_step(a, seqlen), one_step(to, seqlen)))
             return SSM_ERR_ALIAS;
     }
     if (overlaps(y, ybytes, weight, 4 * size_t(dim)) || overlaps(y, ybytes, bias, 4 * size_t(dim)))
@@ -621,8 +622,8 @@ ssm_status_t ssm_group_norm_bwd(int batch, int seqlen, int dim, int groups, ssm_
     if (sums && (!workspace || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
     Steps t[5];
     for (int i = 0; i < 5; ++i)
-        t[i] = {ptrs[i], sp[i] * sizes[i], dim * sizes[i], (long long)(p.step[i] * sizes[i]),
-                (long long)(p.batch[i] * sizes[i])};
+        t[i] = one_step({ptrs[i], sp[i] * sizes[i], dim * sizes[i], (long long)(p.step[i] * sizes[i]),
+                         (long long)(p.batch[i] * sizes[i])}, seqlen);
     auto range = [](const void *ptr, size_t bytes) { return Steps{ptr, bytes, bytes, 0, 0}; };
     const Steps in[] = {t[0], t[1], t[2], range(weight, wb), range(bias, wb)};
     const Steps out[] = {t[3], t[4], range(dweight, wb), range(dbias, wb), range(sums ? workspace : nullptr, need)};

@@ -41,6 +41,13 @@ struct Steps {
     long long step, batch;
 };
 
+// With one step a batch entry the entries are the steps: the step stride of
+// such a tensor says nothing.
+inline Steps one_step(const Steps &a, int seqlen)
+{
+    return seqlen == 1 ? Steps{a.p, a.bytes, a.run, a.batch, 0} : a;
+}
+
 // overlaps(), except that two tensors with the same strides whose runs lie
 // beside each other in every step (slices of one buffer) do not overlap.
 inline bool overlaps(const Steps &a, const Steps &b)

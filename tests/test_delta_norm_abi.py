@@ -181,6 +181,14 @@ def test_slices_of_one_buffer_do_not_overlap():
         assert call_norm(bwd=True, z=fake(23), dx=base, dz=base + off, layout=bad) == ALIAS
 
 
+@pytest.mark.parametrize("step", [0, 200])
+@pytest.mark.parametrize("at", [0, 1, 95, 105, 199, 200])
+def test_slices_of_one_step_that_overlap(step, at):
+    """With one step a batch entry the entries lie a batch stride apart."""
+    lay = delta_layout(ssm.NormBwdLayout, step={3: step, 4: step}, batch={3: 200, 4: 200})
+    assert call_norm(bwd=True, L=1, z=fake(23), dx=fake(24), dz=fake(24) + 2 * at, layout=lay) == ALIAS
+
+
 # ---------------------------------------------------------------- the binding
 def tensors():
     r = torch.randn
