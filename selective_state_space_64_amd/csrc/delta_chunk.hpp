@@ -42,10 +42,10 @@ struct DeltaWs {
 // values), these are composed in order, and then all segments run at once.
 // Sizes only, so that the workspace is known before the call.
 //
-// seg_chunks fills the card once (256 workgroups of 128 columns).  With few
-// heads that would be segments of one chunk, and composing s of them takes
-// s x 12 us of matrix products after one another, while a segment's two runs
-// take 2 x 4.2 us a chunk: about sqrt(chunks) segments are the least time.
+// seg_chunks fills the card once (256 workgroups of 128 columns), but is at
+// least sqrt(chunks): s segments are composed one after another (s x 3.5 us),
+// while a segment's two runs take about 4.2 us a chunk each (16 heads of 4096
+// steps: segments of 4 chunks 136 us, of 8 118; 8 heads of 2048: 78, 91).
 // Only sequences of more than four segments are split, the others lose more
 // to the second run and the two launches than they gain.  Measured, K = V =
 // 128, bf16, split against whole: 40 heads of 16384 steps 684 against 1025 us,

@@ -9,7 +9,11 @@
 // columns (V) of one head's state and all K rows, in registers: a thread 4
 // neighbouring columns of every 256 / (tile / 4)-th row.  The sums over K go
 // through lane moves inside a wave and LDS across the four waves.  A decode
-// step is bound by the state's bytes (2 x 4 K V per head).
+// step is bound by the state's bytes (2 x 4 K V per head): 64 sequences of 40
+// heads, 128 x 128, take 70 us for 336 MB (4.8 TB/s, a large copy's rate), one
+// sequence 11 us, the launch.  Tiles of 32 columns and nontemporal accesses to
+// the state: 16, 32, 64, 128 columns took 119, 67.5, 91, 69 us, and 105 us at 64
+// with ordinary accesses.
 #include "delta_launch.hpp"
 #include "ssm_device.hpp"
 #include "ssm_launch.hpp"
