@@ -125,6 +125,14 @@ def test_split_sequences(case):
     test_forward_and_gradients(case)
 
 
+# enough heads x sequences that eight waves share a workgroup
+@pytest.mark.parametrize("case", [(BF16, [70] * 44, False, 1, 3, 128, 80, {}),
+                                  (BF16, [65, 0, 130] * 12, True, 2, 4, 48, 72, dict(decay="reset"))],
+                         ids=["44 x 3 heads", "packed 36 x 4 heads"])
+def test_many_heads(case):
+    test_forward_and_gradients(case)
+
+
 @pytest.mark.parametrize("case", CASES, ids=name)
 def test_forward_and_gradients(case):
     dtype, lens, packed, hk, h, K, V, opt = case
