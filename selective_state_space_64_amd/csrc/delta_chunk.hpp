@@ -28,7 +28,8 @@ struct DeltaWs {
     // elements a record for one term (the space is for three)
     long long state, step;
     // sequence split (delta_split), per segment and head: end states [KD][Vp],
-    // then the states entering the next segment; transfer matrices' terms [KD][KD]
+    // then the states entering the next segment, and in the last segment's place, which
+    // has neither, the sequence's h0; transfer matrices' terms [KD][KD]
     float *N;
     uint16_t *M;
     int seg_chunks;  // 0: not split
@@ -40,6 +41,8 @@ struct DeltaWs {
 // segment but a sequence's last first yields its end state from zero (or h0)
 // and its K x K transfer matrix (the same recurrence on the unit columns, no
 // values), these are composed in order, and then all segments run at once.
+// That last run reads h0 from the workspace, where the first has copied it: hL
+// may be the same memory, and a last segment may end before a first one begins.
 // Sizes only, so that the workspace is known before the call.
 //
 // seg_chunks fills the card once (256 workgroups of 128 columns), but is at
@@ -141,7 +144,8 @@ inline bool delta_fast(const void *p, const DeltaStride &s, int n, int esize, co
 // What one workgroup runs through: chunks [c0, c1) of a sequence.
 struct DeltaSegment {
     int seq, index, c0, c1;
-    bool live;  // there is such a segment (an empty sequence has one)
+    int behind;  // segments of its sequence after it
+    bool live;   // there is such a segment (an empty sequence has one)
     bool last;  // of its sequence
     DeltaSeq s;
 };
@@ -174,6 +178,7 @@ __device__ inline DeltaSegment delta_segment(const int *cu, int nseq, int seqlen
     d.c1 = seg_chunks ? min(d.c0 + seg_chunks, chunks) : chunks;
     d.live = d.index == 0 || (d.index > 0 && d.c0 < chunks);
     d.last = d.c1 == chunks;
+    d.behind = seg_chunks ? max((chunks + seg_chunks - 1) / seg_chunks - 1 - d.index, 0) : 0;
     return d;
 }
 

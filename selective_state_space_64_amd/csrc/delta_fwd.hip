@@ -268,9 +268,12 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
     const int c0 = seg.c0, chunks = seg.c1;
     const long long state_at = ((long long)seg.seq * p.h + head) * p.K * (long long)p.V + col;
     const long long rec0 = (long long)seq.chunk0 * p.h + head;
-    // this segment's place in N and M, and the state entering it
+    // this segment's place in N and M, and the state entering it: the composed one, h0
+    // as the ends' run kept it, or h0 itself where this workgroup also writes hL
     const long long slot = (long long)blockIdx.z * p.h + head;
+    float *const first_entry = p.ws.N + (slot + (long long)seg.behind * p.h) * p.ws.state + col;
     const float *entry = seg.index ? p.ws.N + (slot - p.h) * p.ws.state + col : nullptr;
+    if (!kEnd && !seg.index && seg.behind && p.h0) entry = first_entry;
 
     Stage st;
     st.init(lds, static_cast<const T *>(p.k) + seq.batch * p.sk.b + seq.first * p.sk.t + (head / p.rep) * p.sk.h, p.sk.t,
@@ -296,6 +299,13 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
             else if (p.h0 && mine && row < p.K) s = p.h0[state_at + (long long)row * p.V];
             S[m][e] = s;
         }
+    if (kEnd && !seg.index && p.h0 && kept) {
+#pragma unroll
+        for (int m = 0; m < KD / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                first_entry[(long long)(32 * (m / 2) + 8 * g + 4 * (m % 2) + e) * p.Vp] = S[m][e];
+    }
 
     Column<T, kFast> lc;
     if (chunks > c0) {
