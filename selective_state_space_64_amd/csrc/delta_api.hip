@@ -57,7 +57,9 @@ bool delta_stride(long long given_t, long long given_h, long long given_b, int b
         span += x.stride * (x.n - 1);
         if (span >= most) return false;
     }
-    s = {(long long)dt, (long long)dh, (long long)db};
+    // the kernels bound a buffer of rows by rows x step: one step's is a row, whatever the
+    // stride that leads to no second one
+    s = {steps == 1 ? row : (long long)dt, (long long)dh, (long long)db};
     sp = size_t(span);
     return true;
 }

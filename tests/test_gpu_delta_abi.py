@@ -1,0 +1,57 @@
+"""Calls of the gated delta rule through its C ABI with strides that the
+binding does not pass on: tensors of one step, whose step stride says nothing."""
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_64_amd as ssm
+from test_gpu_delta import ARGS, BF16, F32, make
+
+pytestmark = pytest.mark.gpu
+
+CODE = {F32: ssm.SSM_F32, BF16: ssm.SSM_BF16}
+
+
+def layout(cls, step):
+    """Dense strides but for the step's."""
+    lay = cls()
+    for i in range(len(lay.step)):
+        lay.step[i] = step
+    return lay
+
+
+def batches(lay, sizes):
+    for i, n in enumerate(sizes):
+        lay.batch[i] = n
+    return ctypes.byref(lay)
+
+
+def run(t, dtype, hk, h, K, V, step):
+    B = t["q"].shape[0]
+    L = ssm.lib()
+    stream = torch.cuda.current_stream().cuda_stream
+    out = {"y": torch.full_like(t["v"], float("nan")), "hL": torch.full_like(t["h0"], float("nan"))}
+    out.update({"d" + n: torch.full_like(t[n], float("nan")) for n in (*ARGS, "h0")})
+    p = {n: x.data_ptr() for n, x in {**t, **out}.items()}
+    need = L.ssm_delta_bwd_workspace_bytes(B, 1, hk, h, K, V, 0)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    qk, vy = hk * K, h * V
+    fwd = batches(layout(ssm.DeltaLayout, step), (qk, qk, vy, vy, h, h))
+    bwd = batches(layout(ssm.DeltaBwdLayout, step), (qk, qk, vy, h, h, vy, qk, qk, vy))
+    head = (B, 1, hk, h, K, V, CODE[dtype], 0, None, *(p[n] for n in ARGS), p["h0"], None, 0, CODE[dtype])
+    assert L.ssm_delta_fwd(*head, p["y"], p["hL"], ws.data_ptr(), need, fwd, stream) == 0
+    assert L.ssm_delta_bwd(*head, p["dy"], p["dhL"], p["dq"], p["dk"], p["dv"], p["dg"], p["dbeta"], p["dh0"],
+                           ws.data_ptr(), need, bwd, stream) == 0
+    return out
+
+
+@pytest.mark.parametrize("step", [1, 8, 64])
+@pytest.mark.parametrize("dtype,hk,h,K,V", [(BF16, 2, 4, 64, 72), (BF16, 1, 1, 128, 128), (F32, 2, 2, 64, 40),
+                                            (BF16, 1, 2, 33, 17)],
+                         ids=["copies", "one head", "runs", "elements"])
+def test_step_stride_of_one_step(dtype, hk, h, K, V, step):
+    t, _, _ = make(dtype, [1, 1, 1], False, hk, h, K, V, seed=step)
+    want, got = (run(t, dtype, hk, h, K, V, s) for s in (0, step))
+    for n in want:
+        assert want[n].isfinite().all() and torch.equal(got[n], want[n]), n
