@@ -348,11 +348,13 @@ __device__ inline uint32_t lds_offset(const void *p)
 // (lds: the same in every lane)
 // The copy wants one wait state behind the write of m0, and five behind a vector
 // instruction that wrote an SGPR of `buf` (readfirstlane, a spill's return): the
-// compiler keeps neither inside an asm block, so the s_nop is there for both.
+// compiler keeps neither inside an asm block, so the s_nop is there for both.  m0 is
+// a reserved register, which the compiler sets anew wherever it needs it: it does not
+// belong on the clobber list.
 __device__ inline void copy_to_lds(sgpr4 buf, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf)
-                 : "memory", "m0");
+                 : "memory");
 }
 // Until at most N of the wave's vector-memory operations are under way (they
 // end in order).
