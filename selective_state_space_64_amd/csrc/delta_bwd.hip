@@ -473,6 +473,7 @@ void delta_grad_kernel(const GradParams p)
                 if (m <= wave) {  // row tile `wave` of dY U^T and dX U^T
                     dP[m] = mma<NG, NS>(yw, au[m & 1], dP[m]);
                     dM[m] = mma<NS, NS>(xw, au[m & 1], dM[m]);
+                    settle();
                 }
                 for_terms<NS, NS>([&](int i, int j) {
 #pragma unroll
@@ -519,6 +520,7 @@ void delta_grad_kernel(const GradParams p)
                             kb.t[n] = read_row<NCH>(kt + n * kTile, 16 * c + r, 4 * b + g);
                         kk[c] = mma<NI, NI>(ka, kb, kk[c]);
                         qk[c] = mma<NI, NI>(qa, kb, qk[c]);
+                        settle();
                     }
             }
 #pragma unroll

@@ -161,6 +161,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && kFast ? 4 : 1)) void d
                         kb.t[n] = read_row<NCH>(kt + n * kTile, 16 * c + r, 4 * b + g);
                     kk[c] = mma<NI, NI>(ka, kb, kk[c]);
                     qk[c] = mma<NI, NI>(qa, kb, qk[c]);
+                    settle();
                 }
         }
     }

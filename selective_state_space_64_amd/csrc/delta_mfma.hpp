@@ -92,6 +92,18 @@ template <int N> __device__ inline Frag<N> split8(f32x4 a, f32x4 b)
 // Keeps the instructions before it before those after it.
 __device__ inline void fence() { __builtin_amdgcn_sched_barrier(0); }
 
+// Ends a block of matrix instructions that some waves skip: ten wait states, after
+// which any result may be read.  The hardware does not wait by itself; the compiler
+// counts the states between a product and its use along the paths through the code,
+// but has missed the short one where such a block is joined (three states of eight
+// in the gradients with shared fp32 keys of more than 128 entries).
+__device__ inline void settle()
+{
+    fence();
+    asm volatile("s_nop 7\n\ts_nop 1");
+    fence();
+}
+
 // Orders what stands before it since the last fence: kReads LDS reads (of the
 // next phase) first, then kMatrix matrix instructions with kValu others behind
 // each.
