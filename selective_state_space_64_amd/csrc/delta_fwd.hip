@@ -608,10 +608,11 @@ __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
 #pragma unroll
                         for (int n = 0; n < NS; ++n) a.t[n] = read_row<NCH>(tile + n * kTile, row, 4 * b + g);
                         N[m] = mma<NS, NS>(a, sb[b], N[m]);
-                    } else {  // one term of M with the terms of S that it keeps
+                    } else {  // one term of M: the pairs that it stands in, as in for_terms
                         const bf16x8 a = read_row<NCH>(tile, row, 4 * b + g);
 #pragma unroll
-                        for (int n = 0; n + first < NS; ++n) N[m] = mfma16(a, sb[b].t[n], N[m]);
+                        for (int n = 0; n < NS; ++n)
+                            if (first + n <= kTermOrder<NS, NS>) N[m] = mfma16(a, sb[b].t[n], N[m]);
                     }
                 }
             }

@@ -44,9 +44,10 @@ template <int N> struct Frag {
 // same way), the small ones are then added to what is left and not rounded at
 // the size of the sum.  Several products' pairs are issued in turn, so that no
 // matrix instruction waits for the one before it.
+template <int NA, int NB> constexpr int kTermOrder = NA == 3 && NB == 3 ? 3 : (NA > NB ? NA : NB) - 1;
 template <int NA, int NB, typename F> __device__ inline void for_terms(F &&f)
 {
-    constexpr int kOrder = NA == 3 && NB == 3 ? 3 : (NA > NB ? NA : NB) - 1;
+    constexpr int kOrder = kTermOrder<NA, NB>;
 #pragma unroll
     for (int o = 0; o <= kOrder; ++o)
 #pragma unroll
