@@ -63,7 +63,8 @@ extern "C" {
  * 2^56 elements or more is SSM_ERR_BAD_SHAPE.
  * Overlap is checked on address ranges, except that tensors with the same
  * step and batch strides may lie beside each other in every step (q, k and v,
- * or dq, dk and dv, as slices of one projection's buffer).
+ * or dq, dk and dv, as slices of one projection's buffer; the larger of the
+ * two strides is then a multiple of the smaller).
  * Index order: q, k, v, y, g, beta.  A NULL layout means all zero.
  */
 typedef struct {

@@ -66,16 +66,18 @@ bool delta_stride(long long given_t, long long given_h, long long given_b, int b
 
 float scale_or_default(const float *scale, int K) { return scale ? *scale : 1.0f / sqrtf(float(K)); }
 
-// A tensor for the overlap check, element strides given; where its heads do
-// not lie inside its steps, or for dense buffers (step 0), the range alone
-// counts.
+// A tensor for the overlap check, element strides given: runs of one step's
+// heads, and the strides from run to run, the smaller first (the batch's in
+// time-major tensors; one that leads nowhere is 0).  Where the heads do not lie
+// inside a run, the range alone counts.
 Steps steps_of(const void *p, size_t span, size_t es, const ssm::DeltaStride &s, int heads, int row, int seqlen,
                int batch)
 {
-    const long long run = (heads - 1) * s.h + row;
-    if (run > (seqlen == 1 ? s.b : s.t)) return {p, span * es, span * es, 0, 0};
-    return one_step({p, span * es, size_t(run) * es, (long long)(s.t * es),
-                                 batch == 1 ? 0 : (long long)(s.b * es)}, seqlen);
+    const long long run = (heads - 1) * s.h + row, t = seqlen > 1 ? s.t : 0, b = batch > 1 ? s.b : 0;
+    const bool time_major = !t || (b && b < t);
+    const long long inner = time_major ? b : t, outer = time_major ? t : b;
+    if (run > inner) return {p, span * es, span * es, 0, 0};
+    return {p, span * es, size_t(run) * es, (long long)(inner * es), (long long)(outer * es)};
 }
 Steps range_of(const void *p, size_t bytes) { return {p, bytes, bytes, 0, 0}; }
 
@@ -251,12 +253,12 @@ ssm_status_t ssm_delta_update(int batch, int qk_heads, int heads, int K, int V,
     const void *const ptr[6] = {q, k, v, y, g, beta};
     const size_t size[6] = {es, es, es, os, 4, 4};
     const size_t sbytes = 4 * size_t(num_slots) * heads * K * V;
-    for (int i = 0; i < 6; ++i) {
-        if (i != 3 && overlaps(y, sp[3] * os, ptr[i], sp[i] * size[i])) return SSM_ERR_ALIAS;
-        if (overlaps(state, sbytes, ptr[i], sp[i] * size[i])) return SSM_ERR_ALIAS;
-    }
-    if (overlaps(y, sp[3] * os, slots, 4 * size_t(batch)) || overlaps(state, sbytes, slots, 4 * size_t(batch)))
-        return SSM_ERR_ALIAS;
+    Steps t[6];
+    for (int i = 0; i < 6; ++i) t[i] = steps_of(ptr[i], sp[i], size[i], s[i], nh[i], row[i], 1, batch);
+    const Steps st = range_of(state, sbytes), sl = range_of(slots, 4 * size_t(batch));
+    for (int i = 0; i < 6; ++i)
+        if ((i != 3 && overlaps(t[3], t[i])) || overlaps(st, t[i])) return SSM_ERR_ALIAS;
+    if (overlaps(t[3], sl) || overlaps(st, sl)) return SSM_ERR_ALIAS;
     const float scale = scale_or_default(scale_p, K);
     ssm::DeltaUpdateArgs a{};
     a.f = ssm::DeltaArgs{batch, 1, qk_heads, heads, K, V, in_t == SSM_BF16, out_t == SSM_BF16, batch, nullptr,

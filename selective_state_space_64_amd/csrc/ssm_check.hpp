@@ -34,7 +34,8 @@ inline bool overlaps(const void *p, size_t pb, const void *q, size_t qb)
 }
 
 // A strided tensor in bytes: runs of `run` bytes (one step), `step` apart,
-// batch entries `batch` apart, `bytes` from the first to the last.
+// batch entries `batch` apart, `bytes` from the first to the last.  Of a
+// time-major tensor `step` and `batch` are the other way round.
 struct Steps {
     const void *p;
     size_t bytes, run;
