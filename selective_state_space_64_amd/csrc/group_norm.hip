@@ -502,6 +502,13 @@ bool norm_strides(long long given_step, long long given_batch, int batch, int se
     return true;
 }
 
+// Tensor i for the overlap check; the batch stride of one entry leads nowhere.
+Steps norm_steps(const void *ptr, size_t span, size_t es, const NormParams &p, int i, int batch, int seqlen, int dim)
+{
+    return one_step({ptr, span * es, dim * es, (long long)(p.step[i] * es),
+                     batch == 1 ? 0 : (long long)(p.batch[i] * es)}, seqlen);
+}
+
 // All of the call's tensors admit 16-byte accesses at every run of 8 channels.
 bool norm_vec(const NormParams &p, const void *const *ptrs, const size_t *es, int count, int batch)
 {
@@ -560,10 +567,10 @@ ssm_status_t ssm_group_norm_fwd(int batch, int seqlen, int dim, int groups, ssm_
     // y in place of x or z: every element is read before it is written, by the same thread
     for (int i = 0; i < 2; ++i) {
         const void *in = i ? z : x;
-        const bool same = in == y && in_t == out_t && p.step[i] == p.step[3] && p.batch[i] == p.batch[3];
-        const Steps a{in, sp[i] * es, dim * es, (long long)(p.step[i] * es), (long long)(p.batch[i] * es)};
-        const Steps to{y, ybytes, dim * os, (long long)(p.step[3] * os), (long long)(p.batch[3] * os)};
-        if (!same && overlaps(one_step(a, seqlen), one_step(to, seqlen)))
+        const bool same = in == y && in_t == out_t && (seqlen == 1 || p.step[i] == p.step[3]) &&
+                          (batch == 1 || p.batch[i] == p.batch[3]);
+        if (!same && overlaps(norm_steps(in, sp[i], es, p, i, batch, seqlen, dim),
+                              norm_steps(y, sp[2], os, p, 3, batch, seqlen, dim)))
             return SSM_ERR_ALIAS;
     }
     if (overlaps(y, ybytes, weight, 4 * size_t(dim)) || overlaps(y, ybytes, bias, 4 * size_t(dim)))
@@ -629,8 +636,7 @@ ssm_status_t ssm_group_norm_bwd(int batch, int seqlen, int dim, int groups, ssm_
     if (sums && (!workspace || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
     Steps t[5];
     for (int i = 0; i < 5; ++i)
-        t[i] = one_step({ptrs[i], sp[i] * sizes[i], dim * sizes[i], (long long)(p.step[i] * sizes[i]),
-                         (long long)(p.batch[i] * sizes[i])}, seqlen);
+        t[i] = norm_steps(ptrs[i], sp[i], sizes[i], p, i, batch, seqlen, dim);
     auto range = [](const void *ptr, size_t bytes) { return Steps{ptr, bytes, bytes, 0, 0}; };
     const Steps in[] = {t[0], t[1], t[2], range(weight, wb), range(bias, wb)};
     const Steps out[] = {t[3], t[4], range(dweight, wb), range(dbias, wb), range(sums ? workspace : nullptr, need)};

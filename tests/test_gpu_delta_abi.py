@@ -1,5 +1,6 @@
-"""Calls of the gated delta rule through its C ABI with strides that the
-binding does not pass on: tensors of one step, whose step stride says nothing."""
+"""Calls of the gated delta rule and of the grouped norm through their C ABI
+with strides that the binding does not pass on: of tensors of one step or one
+batch entry, where they say nothing."""
 import ctypes
 
 import pytest
@@ -55,3 +56,27 @@ def test_step_stride_of_one_step(dtype, hk, h, K, V, step):
     want, got = (run(t, dtype, hk, h, K, V, s) for s in (0, step))
     for n in want:
         assert want[n].isfinite().all() and torch.equal(got[n], want[n]), n
+
+
+def test_norm_batch_stride_of_one_entry():
+    """dx and dz beside each other in the rows of one batch entry, whose batch
+    strides lead nowhere and differ."""
+    L, dim, groups = 5, 96, 4
+    x, z, dy = (torch.randn(1, L, dim, device="cuda") for _ in range(3))
+    want = ssm.ssm_group_norm_bwd(x, groups, dy, z=z)
+    both = torch.zeros(L, 2 * dim, device="cuda")
+    lay = ssm.NormBwdLayout()
+    lay.step[3] = lay.step[4] = 2 * dim
+    lay.batch[3], lay.batch[4] = 2 * dim * L, 2 * dim * L + 7
+    assert ssm.lib().ssm_group_norm_bwd(
+        1, L, dim, groups, ssm.SSM_F32, 0, None, x.data_ptr(), None, None, z.data_ptr(), ssm.SSM_F32, dy.data_ptr(),
+        both.data_ptr(), both[:, dim:].data_ptr(), None, None, None, 0, ctypes.byref(lay),
+        torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(both, torch.cat([want["dx"][0], want["dz"][0]], -1))
+    want = ssm.ssm_group_norm_fwd(x, groups)  # and y in place of x
+    lay = ssm.NormLayout()
+    lay.batch[2] = dim * L + 7
+    assert ssm.lib().ssm_group_norm_fwd(
+        1, L, dim, groups, ssm.SSM_F32, 0, None, x.data_ptr(), None, None, None, ssm.SSM_F32, x.data_ptr(),
+        ctypes.byref(lay), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(x, want)
