@@ -10,10 +10,8 @@
 // neighbouring columns of every 256 / (tile / 4)-th row.  The sums over K go
 // through lane moves inside a wave and LDS across the four waves.  A decode
 // step is bound by the state's bytes (2 x 4 K V per head): 64 sequences of 40
-// heads, 128 x 128, take 70 us for 336 MB (4.8 TB/s, a large copy's rate), one
-// sequence 11 us, the launch.  Tiles of 32 columns and nontemporal accesses to
-// the state: 16, 32, 64, 128 columns took 119, 67.5, 91, 69 us, and 105 us at 64
-// with ordinary accesses.
+// heads, 128 x 128, take 70.8 us a call for 336 MB (4.8 TB/s, a large copy's
+// rate), one sequence 11 us, the host's part of the call.
 #include "delta_launch.hpp"
 #include "ssm_device.hpp"
 #include "ssm_launch.hpp"
@@ -176,8 +174,9 @@ hipError_t launch_rows(const StepParams &p, int batch, bool vec, hipStream_t str
 template <typename T, typename TOut, int kCols>
 hipError_t launch_cols(const StepParams &p, int batch, bool vec, hipStream_t stream)
 {
-    constexpr int down = kThreads / (kCols / 4);
-    if (p.K <= down) return launch_rows<T, TOut, kCols, 1>(p, batch, vec, stream);
+    constexpr int down = kThreads / (kCols / 4);  // 16 columns: 64, and K is over 64 (launch_typed)
+    if constexpr (kCols == 32)
+        if (p.K <= down) return launch_rows<T, TOut, kCols, 1>(p, batch, vec, stream);
     if (p.K <= 2 * down) return launch_rows<T, TOut, kCols, 2>(p, batch, vec, stream);
     if (p.K <= 4 * down) return launch_rows<T, TOut, kCols, 4>(p, batch, vec, stream);
     if constexpr (down * 4 < kDeltaMaxK) return launch_rows<T, TOut, kCols, 8>(p, batch, vec, stream);
@@ -187,14 +186,15 @@ hipError_t launch_cols(const StepParams &p, int batch, bool vec, hipStream_t str
 template <typename T, typename TOut>
 hipError_t launch_typed(const StepParams &p, int batch, bool vec, hipStream_t stream)
 {
-    // Tiles of 32 columns move the most bytes a second; 16 where those would
-    // leave compute units without work.  64 states of 40 heads of 128 x 128, out
-    // of memory: 16 columns 119 us, 32 67.5, 64 91, 128 69 (336 MB; a copy of as
-    // many bytes 69 us); 74 us with 32 columns and ordinary in place of
-    // nontemporal accesses.
-    const long long wide = (long long)((p.V + 31) / 32) * p.h * batch;
-    return wide >= 1024 ? launch_cols<T, TOut, 32>(p, batch, vec, stream)
-                        : launch_cols<T, TOut, 16>(p, batch, vec, stream);
+    // Tiles of 32 columns move the most bytes a second; 16 give twice the workgroups,
+    // each with half as long a column of the state to a thread, where the card is far from
+    // full.  us a step in a graph, states out of memory, 32 against 16 columns, by tiles of
+    // 32: K = 64 3.65 / 4.02 at 64 tiles, 3.9 / 5.1 at 256; K = 128 5.7 / 4.4 at 64, 5.9 / 5.5 at
+    // 192, 6.0 / 6.0 at 256, 6.5 / 7.2 at 384, 8.0 / 12.6 at 960, 35 / 55 at 5120; K = 256 9.1 / 6.5
+    // at 64, 9.6 / 8.4 at 256, 11.1 / 12.7 at 512, 20.0 / 18.4 at 768, 21.1 / 24.5 at 1024.
+    const long long tiles = (long long)((p.V + 31) / 32) * p.h * batch;
+    return p.K <= 64 || tiles >= 2 * p.K ? launch_cols<T, TOut, 32>(p, batch, vec, stream)
+                                         : launch_cols<T, TOut, 16>(p, batch, vec, stream);
 }
 
 }  // namespace
