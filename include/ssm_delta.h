@@ -32,9 +32,16 @@
  *     covers keep what the outputs held.  A sequence may be empty: its hL is
  *     its h0 (or zero).
  *   - Arithmetic: products run on the matrix cores with every operand that
- *     is not exact in bf16 split into two or three bf16 terms, sums and the
- *     state are fp32.  g is any real number or -inf (the state is cleared);
- *     below -110 it acts as -110 (e^-110 is 0 in fp32).
+ *     is not exact in bf16 split into bf16 terms, sums and the running state are
+ *     fp32.  bf16 inputs: two terms (16 bits of significand); a bf16 y or gradient
+ *     does not show it, fp32 outputs have relative errors of about 4e-6.  fp32
+ *     inputs: three terms (24 bits), errors of fp32 arithmetic; a caller who wants
+ *     those of bf16 values passes them as fp32 (y and the gradients may still be
+ *     bf16).  The decode step computes in fp32 throughout.
+ *   - g is a log decay: a real number or -inf (the state is cleared); below -110
+ *     it acts as -110 (e^-110 is 0 in fp32).  Where g grows instead of decaying,
+ *     its sums over neighbouring steps of a 64-step chunk have to stay below 88
+ *     (e^88 is the largest power that fp32 holds).
  *   - A non-finite q, k, v or beta reaches the outputs of its own head and
  *     sequence from the start of its 64-step chunk on (steps are combined a
  *     chunk at a time); other sequences and heads are not touched by it.

@@ -22,9 +22,10 @@
 //            - beta_i e^{G_i} k_i.(dX S0^T)_i) + sum_{j < m} tail_j k_j.(U dS1^T)_j
 //            + e^{Gc} <S0, dS1>,      W = dP (Q K^T) + N (K K^T)
 //
-// Measured with 4 x 40 heads of 128 x 128, 2048 steps, bf16 (986 us a training
-// step with the forward's 90 + 260 us): the reverse recurrence 280 us, the
-// gradients 390 us.  Both are bound by the records between them: S0 and dS1 of
+// Measured with 4 x 40 heads of 128 x 128, 2048 steps, bf16: 986 us a training
+// step.  By the profiler (a few us longer for each kernel) the forward's part takes
+// 90 + 255 us, the reverse recurrence 286 us and the gradients 399 us.
+// Both are bound by the records between them: S0 and dS1 of
 // two terms are 64 KB each a chunk and head, 330 MB each here, and U and dX
 // another 170 MB each, written once and read once (410 us of the 986 at the
 // rate of a large copy); recomputing S0 from fewer kept chunks would trade them
@@ -38,8 +39,8 @@ namespace {
 constexpr int kThreads = 256;
 
 // bf16 terms of dY
-template <typename T, typename TG, int KD>
-constexpr int kGradTerms = sizeof(TG) == 2 ? 1 : Terms<T, KD>::kSum;
+template <typename T, typename TG>
+constexpr int kGradTerms = sizeof(TG) == 2 ? 1 : Terms<T>::kSum;
 
 template <typename TG> __device__ inline void store_grad(TG *p, float v)
 {
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 {
     constexpr bool kFast = kPath >= kByRun, kAsync = kPath == kByCopy;
     using Stage = ChunkStage<T, KD, kWaves, kFast, kAsync, true, true>;
-    constexpr int NI = Stage::NI, NS = Stage::NS, NG = kGradTerms<T, TG, KD>;
+    constexpr int NI = Stage::NI, NS = Stage::NS, NG = kGradTerms<T, TG>;
     constexpr int NCH = Stage::NCH, kTile = Stage::kTile, KB = KD / 32;
     constexpr int kKept = (KB + 2) * NS;  // stores of a chunk beside dv's 16
     __shared__ __align__(16) uint16_t lds[Stage::kBuffers * Stage::kBuffer];
@@ -338,7 +339,7 @@ template <typename T, typename TG, int KD, bool kShared, bool kFast>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && KD <= 128 && !kShared ? 2 : 1))
 void delta_grad_kernel(const GradParams p)
 {
-    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum, NG = kGradTerms<T, TG, KD>;
+    constexpr int NI = Terms<T>::kIn, NS = Terms<T>::kSum, NG = kGradTerms<T, TG>;
     constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;  // K and Q are staged KH columns at a time
     constexpr int kHalves = KD / KH, NT = KH / 64, NTT = KD / 64, KB = KD / 32;  // NTT column tiles a wave
     // LDS: 32 value columns of S0, dS1, U, dX, dY and V, then K, Q and the 64 x 64 matrices

@@ -18,10 +18,11 @@
 // share only the chunk's K, Q, T, P (and V) in LDS, which bf16 rows reach by
 // copies that pass no register, a chunk ahead.
 //
-// Measured with 4 x 40 heads of 128 x 128, 2048 steps, bf16 (215 us a call):
-// the chunks' matrices 70 us (the longest is the triangular inverse, products
-// of 16 x 16 blocks after one another), the recurrence 160 us where its reads
-// and writes alone would take 70.  No one thing bounds it: the matrix pipe is
+// Measured with 4 x 40 heads of 128 x 128, 2048 steps, bf16: 221 us a call.  By
+// the profiler, under which each kernel takes a few us longer than its part of a
+// call, the chunks' matrices take 71 us (the longest is the triangular inverse,
+// products of 16 x 16 blocks after one another) and the recurrence 162 us, where
+// the call's reads and writes alone would take 70.  No one thing bounds it: the matrix pipe is
 // busy for about 36 % of it, LDS for 50 %, the vector ALU (conversions to
 // terms) for 40 %, and taking any one phase away gains at most 30 us; the chain of
 // products of a chunk (K S0, T X, P U, K^T U) leaves each wave waiting for its
@@ -84,13 +85,13 @@ __device__ inline void write_tri(const float *m, int diag, uint16_t *out)
     }
 }
 
-// 4 x 40 heads, 32 chunks of 64 x 128 in bf16 (168 MB in): 70 us, with the
-// transposes for the backward pass 90 us; bound by the inverse's chain, so four
-// workgroups share a compute unit.
+// 4 x 40 heads, 32 chunks of 64 x 128 in bf16 (168 MB in): 71 us by the
+// profiler, with the transposes for the backward pass 90 us; bound by the
+// inverse's chain, so four workgroups share a compute unit.
 template <typename T, int KD, bool kBoth, bool kFast>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && kFast ? 4 : 1)) void delta_prep_kernel(const PrepParams p)
 {
-    constexpr int NI = Terms<T, KD>::kIn, NS = Terms<T, KD>::kSum;
+    constexpr int NI = Terms<T>::kIn, NS = Terms<T>::kSum;
     constexpr int KH = KD < 128 ? KD : 128, NCH = KH / 8, kTile = 64 * KH;
     constexpr int kTiles = 2 * NI * kTile * 2, kMats = 2 * 64 * kPitch * 4;
     __shared__ __align__(16) unsigned char lds[kTiles > kMats ? kTiles : kMats];
@@ -540,11 +541,11 @@ __global__ __launch_bounds__(64 * kWaves, (kWaves == 8 ? 2 : 1)) void delta_scan
 // N_s.  entry_1 is N_0.  A wave holds 16 columns, as in the recurrence; M's
 // terms come to LDS for the workgroup's four waves, a segment ahead where two
 // of them fit.  A chain of products, 3 to 4 us a segment (12 heads of 65521
-// steps in 21 segments: 74 us of 850).
+// steps in 21 segments: 74 us of 850 to 890).
 template <typename T, int KD>
 __global__ __launch_bounds__(256) void delta_compose_kernel(const ScanParams p)
 {
-    constexpr int NS = Terms<T, KD>::kSum, NCH = KD / 8, KB = KD / 32, kTile = KD * KD;
+    constexpr int NS = Terms<T>::kSum, NCH = KD / 8, KB = KD / 32, kTile = KD * KD;
     constexpr int kPlanes = KD > 128 ? 1 : NS;  // of M in LDS at a time
     constexpr int kBuffers = 2 * kPlanes * kTile * 2 <= 160 * 1024 ? 2 : 1;
     __shared__ __align__(16) uint16_t lds[kBuffers * kPlanes * kTile];

@@ -10,7 +10,7 @@
 // neighbouring columns of every 256 / (tile / 4)-th row.  The sums over K go
 // through lane moves inside a wave and LDS across the four waves.  A decode
 // step is bound by the state's bytes (2 x 4 K V per head): 64 sequences of 40
-// heads, 128 x 128, take 70.8 us a call for 336 MB (4.8 TB/s, a large copy's
+// heads, 128 x 128, take 70.4 us a call for 336 MB (4.8 TB/s, a large copy's
 // rate), one sequence 11 us, the host's part of the call.
 #include "delta_launch.hpp"
 #include "ssm_device.hpp"

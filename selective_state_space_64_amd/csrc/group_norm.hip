@@ -18,12 +18,16 @@
 // 16-byte accesses do not fit) take one workgroup each and read x again per
 // pass, from the L2.
 //
-// Measured: 4 x 2048 steps of 5120 channels in 40 groups, bf16 with a gate, 53 us
-// for 252 MB (4.8 TB/s, a large copy's rate), the gradients 94 us for 419 MB
-// (4.5 TB/s); a workgroup a row of several groups, so that small groups still
-// make whole 16-byte lines.  Small calls are bound by the launch (8 x 1536: 11 us).
-// The gradients' partial rows are one per workgroup and channel, added by the
-// second kernel in about 4 us; more or fewer of them made no difference.
+// Measured, calls on tensors out of memory: 4 x 2048 steps of 5120 channels in 40
+// groups, bf16 with a gate, 53 us for 252 MB (4.7 TB/s, a large copy's rate), the
+// gradients with their second kernel 94 us for 419 MB (4.5 TB/s); a workgroup a row
+// of several groups, so that small groups still make whole 16-byte lines.  Small
+// calls are bound by the host's part of them (8 x 1536: 11 us).  The gradients'
+// partial rows are one per workgroup and channel, added by the second kernel in 5 us
+// (by the profiler); more or fewer of them made no difference.  The long groups are far
+// from the floor: one group of 5120 bf16 channels, gated, 142 us where 52 are the bytes',
+// the gradients 646 us against 86 (three passes over each row, and the sums of every
+// row added to the partial rows in memory).
 #include "ssm_norm.h"
 
 #include "ssm_check.hpp"
