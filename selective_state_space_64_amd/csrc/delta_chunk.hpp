@@ -21,10 +21,11 @@ inline int delta_vp(int V) { return (V + 63) / 64 * 64; }
 // fp32 arithmetic has 1e-7 to 4e-7.  A caller who wants these passes the same
 // values as fp32 (an exact conversion; the outputs may still be bf16): errors of 1.1e-7
 // to 3.4e-7 for the layer of 4 x 40 heads, at 976 us against 220 forward and 2.99 ms
-// against 0.99 for a training step.  Three terms for bf16 inputs in the update of the
-// state alone were measured too: hL 1.1e-6, dh0 0.9e-6, dg and dbeta as before, the
-// forward 3.7 % slower; in all products two buffers do not fit 160 KB of LDS with eight
-// waves.
+// against 0.99 for a training step.  Three terms for bf16 inputs were measured too: in
+// the update of the state alone hL 1.1e-6 and dh0 0.9e-6 with a forward 3.7 % slower, in
+// T X as well hL 3.2e-7 with a forward 11 to 15 % slower (5 % a training step), dg and
+// dbeta as before in both; in all products two buffers do not fit 160 KB of LDS with
+// eight waves.
 template <typename T> struct Terms {
     static constexpr int kIn = sizeof(T) == 2 ? 1 : 3;
     static constexpr int kSum = sizeof(T) == 2 ? 2 : 3;
