@@ -59,13 +59,15 @@ extern "C" {
 
 #define SSM_ABI_VERSION 1
 
-typedef enum { SSM_F32 = 0, SSM_BF16 = 1 } ssm_dtype_t;
+/* SSM_E4M3 (8 bits, OCP e4m3 without infinities) is an output type of
+ * ssm_rms_norm_fwd and SSM_ERR_BAD_DTYPE everywhere else. */
+typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_E4M3 = 2 } ssm_dtype_t;
 
 typedef enum {
     SSM_OK = 0,
     SSM_ERR_NULL_ARG = 1,    /* a required pointer is NULL                         */
     SSM_ERR_BAD_SHAPE = 2,   /* a size < 1 or beyond the supported range (below)    */
-    SSM_ERR_BAD_DTYPE = 3,   /* in_dtype or out_dtype is not a value of ssm_dtype_t */
+    SSM_ERR_BAD_DTYPE = 3,   /* a type argument is not one that the call takes      */
     SSM_ERR_MISALIGNED = 4,  /* a pointer below its element alignment (state: 16 B) */
     SSM_ERR_ALIAS = 5,       /* an output overlaps an input it must not overlap    */
     SSM_ERR_UNSUPPORTED = 6, /* dstate not in {1,2,4,8,16}, or an unknown flag bit   */

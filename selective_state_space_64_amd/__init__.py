@@ -1,8 +1,8 @@
 """Selective state-space (S6) scan for AMD MI355X (gfx950).
 
 Thin Python binding over the C ABI in ``include/ssm.h``, ``include/ssm_bwd.h``,
-``include/ssm_conv.h``, ``include/ssm_delta.h`` and ``include/ssm_norm.h``
-(``libssm.so``): argument marshalling only.  Every step of the computation runs in the HIP
+``include/ssm_conv.h``, ``include/ssm_delta.h``, ``include/ssm_norm.h``,
+``include/ssm_heads.h`` and ``include/ssm_rms.h`` (``libssm.so``): argument marshalling only.  Every step of the computation runs in the HIP
 kernels of ``csrc/``; PyTorch only provides device memory and the stream.
 There is no CPU fallback: if the library is missing or no GPU is present the
 calls raise.
@@ -17,6 +17,11 @@ calls raise.
     y = ssm_delta_update(state, q, k, v, g, beta, scale=..., slots=...)
     y = ssm_group_norm_fwd(x, groups, weight=..., bias=..., z=..., rms=..., silu=...)
     grads = ssm_group_norm_bwd(x, groups, dy, weight=..., bias=..., z=...)
+    y, hL = ssm_head_scan_fwd(x, dt, A, Bm, Cm, Dskip=..., dt_bias=..., h0=..., cu_seqlens=...)
+    grads = ssm_head_scan_bwd(x, dt, A, Bm, Cm, dy, Dskip=..., dt_bias=..., h0=..., dhL=...)
+    y = ssm_head_scan_update(state, x, dt, A, Bm, Cm, Dskip=..., dt_bias=..., slots=...)
+    y, h, scales = ssm_rms_norm_fwd(x, weight=..., residual=..., out_dtype=...)
+    grads = ssm_rms_norm_bwd(h, dy, weight=..., dh=...)
 
 Layouts: x, dt, z, y [batch, dim, L]; Bm, Cm [batch, N, L]; A [dim, N];
 Dskip, dt_bias [dim]; h0, hL, state [batch, dim, N] (decode: drop L);
@@ -24,6 +29,9 @@ conv weight [dim, W], bias [dim], conv state [batch, dim, W-1].
 Gated delta rule: q, k [batch, L, qk_heads, K]; v, y [batch, L, heads, V];
 g, beta [batch, L, heads]; states [sequences, heads, K, V] (decode: drop L).
 Grouped norm: x, z, y [batch, L, dim] or [batch, dim].
+Head scan: x, y [batch, L, heads, P]; dt [batch, L, heads]; Bm, Cm
+[batch, L, groups, N]; A, Dskip, dt_bias [heads]; states [sequences, heads, N,
+P] (decode: drop L).  Residual norm: as the grouped norm.
 """
 import ctypes
 import functools
@@ -34,7 +42,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libssm.so")
 
-SSM_F32, SSM_BF16 = 0, 1
+SSM_F32, SSM_BF16, SSM_E4M3 = 0, 1, 2
 SSM_FLAG_ZOH_B = 0x1
 SSM_FLAG_CHECKPOINTS = 0x2
 SSM_CONV_SILU = 0x1
@@ -54,7 +62,10 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_fwd_workspace_bytes
            "ssm_scan_bwd_bld_workspace_bytes", "ssm_scan_bwd_bld",
            "ssm_delta_fwd_workspace_bytes", "ssm_delta_fwd",
            "ssm_delta_bwd_workspace_bytes", "ssm_delta_bwd", "ssm_delta_update",
-           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_bytes", "ssm_group_norm_bwd"]
+           "ssm_group_norm_fwd", "ssm_group_norm_bwd_workspace_bytes", "ssm_group_norm_bwd",
+           "ssm_head_scan_fwd_workspace_bytes", "ssm_head_scan_fwd",
+           "ssm_head_scan_bwd_workspace_bytes", "ssm_head_scan_bwd", "ssm_head_scan_update",
+           "ssm_rms_norm_fwd", "ssm_rms_norm_bwd_workspace_bytes", "ssm_rms_norm_bwd"]
 
 
 class ScanLayout(ctypes.Structure):
@@ -120,6 +131,29 @@ class NormLayout(ctypes.Structure):
 
 class NormBwdLayout(ctypes.Structure):
     """ssm_norm_bwd_layout_t: the same for x, z, dy, dx, dz."""
+    _fields_ = [(n, ctypes.c_longlong * 5) for n in ("step", "batch")]
+
+
+class HeadScanLayout(ctypes.Structure):
+    """ssm_head_scan_layout_t: step, head and batch strides in elements of x,
+    dt, Bm, Cm, y, 0 = dense default."""
+    _fields_ = [(n, ctypes.c_longlong * 5) for n in ("step", "head", "batch")]
+
+
+class HeadScanBwdLayout(ctypes.Structure):
+    """ssm_head_scan_bwd_layout_t: the same for x, dt, Bm, Cm, dy, dx, ddt, dBm, dCm."""
+    _fields_ = [(n, ctypes.c_longlong * 9) for n in ("step", "head", "batch")]
+
+
+class RmsLayout(ctypes.Structure):
+    """ssm_rms_layout_t: step and batch strides of x, residual, residual_out, y,
+    and the scales' strides, 0 = dense default."""
+    _fields_ = ([(n, ctypes.c_longlong * 4) for n in ("step", "batch")]
+                + [(n, ctypes.c_longlong) for n in ("scale_step", "scale_batch", "scale_block")])
+
+
+class RmsBwdLayout(ctypes.Structure):
+    """ssm_rms_bwd_layout_t: step and batch strides of h, dy, dh, dx, dresidual."""
     _fields_ = [(n, ctypes.c_longlong * 5) for n in ("step", "batch")]
 
 
@@ -205,6 +239,21 @@ def lib():
         L.ssm_group_norm_bwd_workspace_bytes.argtypes = [i] * 4
         L.ssm_group_norm_bwd.restype = i
         L.ssm_group_norm_bwd.argtypes = [i] * 5 + [u, vp] + [vp] * 4 + [i] + [vp] * 6 + [sz, vp, vp]
+        for name in ("ssm_head_scan_fwd_workspace_bytes", "ssm_head_scan_bwd_workspace_bytes"):
+            getattr(L, name).restype = sz
+            getattr(L, name).argtypes = [i] * 7
+        L.ssm_head_scan_fwd.restype = i
+        L.ssm_head_scan_fwd.argtypes = [i] * 7 + [u] + [vp] * 9 + [i, i] + [vp] * 3 + [sz, vp, vp]
+        L.ssm_head_scan_bwd.restype = i
+        L.ssm_head_scan_bwd.argtypes = [i] * 7 + [u] + [vp] * 9 + [i, i] + [vp] * 11 + [sz, vp, vp]
+        L.ssm_head_scan_update.restype = i
+        L.ssm_head_scan_update.argtypes = [i] * 6 + [vp, i] + [vp] * 8 + [i, vp, vp, vp]
+        L.ssm_rms_norm_fwd.restype = i
+        L.ssm_rms_norm_fwd.argtypes = [i] * 5 + [vp] * 5 + [i] + [vp] * 4
+        L.ssm_rms_norm_bwd_workspace_bytes.restype = sz
+        L.ssm_rms_norm_bwd_workspace_bytes.argtypes = [i] * 3
+        L.ssm_rms_norm_bwd.restype = i
+        L.ssm_rms_norm_bwd.argtypes = [i] * 5 + [vp] * 9 + [sz, vp, vp]
         _lib = L
     return _lib
 
@@ -1095,6 +1144,264 @@ def ssm_group_norm_bwd(x, groups, dy, *, weight=None, bias=None, z=None, eps=Non
     return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
 
 
+@_plan
+def _head_scan_sizes(x, Bm, cu):
+    if len(x[1]) != 4 or len(Bm[1]) != 4:
+        raise ValueError("x must be [batch, L, heads, P] and Bm [batch, L, groups, N]")
+    if cu is not None and (len(cu[1]) != 1 or cu[3] != torch.int32 or cu[1][0] < 2):
+        raise TypeError("cu_seqlens must be an int32 tensor of (sequences + 1) entries")
+    (batch, L, H, P), (G, N) = x[1], Bm[1][2:]
+    return batch, L, G, H, N, P, cu[1][0] - 1 if cu is not None else 0
+
+
+@_plan
+def _head_scan_fwd_plan(x, dt, A, Bm, Cm, Dskip, dt_bias, y, h0, hL, cu, ws, out_dtype):
+    every = (x, dt, A, Bm, Cm, Dskip, dt_bias, y, h0, hL, cu, ws)
+    _whole(*every)
+    sizes = batch, L, G, H, N, P, nseq = _head_scan_sizes(x, Bm, cu)
+    ind, f32, state = x[3], torch.float32, (nseq or batch, H, N, P)
+    out_dtype = y[3] if y is not None else out_dtype or ind
+    xy, bc = (batch, L, H, P), (batch, L, G, N)
+    layout = _layout(HeadScanLayout, _BTH, (x, xy, ind), (dt, xy[:3], ind), (Bm, bc, ind), (Cm, bc, ind),
+                     (y, xy, out_dtype))
+    _dense(*[(m, (H,), f32) for m in (A, Dskip, dt_bias)], (h0, state, f32), (hL, state, f32), (cu, None, None),
+           (ws, None, None))
+    _on_gpu(*every)
+    need = lib().ssm_head_scan_fwd_workspace_bytes(*sizes)
+    return sizes, _dtype_code(ind), _dtype_code(out_dtype), out_dtype, state, need, ctypes.byref(layout)
+
+
+@_plan
+def _head_scan_bwd_plan(x, dt, A, Bm, Cm, dy, Dskip, dt_bias, h0, dhL, cu, ws, dx, ddt, dBm, dCm):
+    every = (x, dt, A, Bm, Cm, dy, Dskip, dt_bias, h0, dhL, cu, ws, dx, ddt, dBm, dCm)
+    _whole(*every)
+    sizes = batch, L, G, H, N, P, nseq = _head_scan_sizes(x, Bm, cu)
+    ind, gt, f32, state = x[3], dy[3], torch.float32, (nseq or batch, H, N, P)
+    xy, bc = (batch, L, H, P), (batch, L, G, N)
+    layout = _layout(HeadScanBwdLayout, _BTH, (x, xy, ind), (dt, xy[:3], ind), (Bm, bc, ind), (Cm, bc, ind),
+                     (dy, xy, gt), (dx, xy, gt), (ddt, xy[:3], gt), (dBm, bc, gt), (dCm, bc, gt))
+    _dense(*[(m, (H,), f32) for m in (A, Dskip, dt_bias)], (h0, state, f32), (dhL, state, f32), (cu, None, None),
+           (ws, None, None))
+    _on_gpu(*every)
+    return sizes, _dtype_code(ind), _dtype_code(gt), state, ctypes.byref(layout)
+
+
+@_plan
+def _head_scan_update_plan(state, x, dt, A, Bm, Cm, Dskip, dt_bias, y, slots, out_dtype):
+    every = (state, x, dt, A, Bm, Cm, Dskip, dt_bias, y, slots)
+    _whole(*every)
+    if len(x[1]) != 3 or len(Bm[1]) != 3 or len(state[1]) != 4:
+        raise ValueError("x must be [batch, heads, P], Bm [batch, groups, N], state [slots, heads, N, P]")
+    (batch, H, P), (G, N) = x[1], Bm[1][1:]
+    ind, f32 = x[3], torch.float32
+    out_dtype = y[3] if y is not None else out_dtype or ind
+    if slots is None and state[1][0] != batch:
+        raise ValueError("state has %d entries for %d rows (pass slots)" % (state[1][0], batch))
+    xy, bc = (batch, H, P), (batch, G, N)
+    layout = _layout(HeadScanLayout, ("batch", "head"), (x, xy, ind), (dt, xy[:2], ind), (Bm, bc, ind), (Cm, bc, ind),
+                     (y, xy, out_dtype))
+    _dense(*[(m, (H,), f32) for m in (A, Dskip, dt_bias)], (state, (state[1][0], H, N, P), f32),
+           (slots, (batch,), torch.int32))
+    _on_gpu(*every)
+    return ((batch, G, H, N, P, _dtype_code(ind)), state[1][0], _dtype_code(out_dtype), out_dtype, xy,
+            ctypes.byref(layout))
+
+
+def ssm_head_scan_bwd_workspace(x, Bm, *, cu_seqlens=None):
+    """A device buffer of ssm_head_scan_bwd_workspace_bytes(...) bytes for these
+    inputs: `checkpoints` of ssm_head_scan_fwd and `workspace` of ssm_head_scan_bwd."""
+    need = lib().ssm_head_scan_bwd_workspace_bytes(*_head_scan_sizes(*_meta(x=x, Bm=Bm, cu_seqlens=cu_seqlens)))
+    return torch.empty(max(1, need), dtype=torch.uint8, device=x.device)
+
+
+@_on_caller_stream
+def ssm_head_scan_fwd(x, dt, A, Bm, Cm, *, Dskip=None, dt_bias=None, h0=None, cu_seqlens=None, out_dtype=None,
+                      return_final_state=True, y=None, hL=None, checkpoints=None, workspace=None, stream=None):
+    """The selective scan with one decay a head over whole sequences; returns
+    (y, hL).  x and y [batch, L, heads, P], dt [batch, L, heads], Bm and Cm
+    [batch, L, groups, N], in any order of the first three strides (slices of
+    one conv output); A (negative), Dskip, dt_bias [heads] fp32; h0, hL
+    [sequences, heads, N, P] fp32.  The step size is softplus(dt + dt_bias),
+    out_dtype defaults to x's dtype.
+    cu_seqlens: int32 device tensor of sequence bounds for sequences packed
+    into one batch row.  checkpoints: a buffer from ssm_head_scan_bwd_workspace
+    that receives what ssm_head_scan_bwd reads (checkpoints_in_workspace=True).
+    hL may be h0 (the state moves on in place)."""
+    ws = checkpoints if checkpoints is not None else workspace
+    sizes, code, out_code, out_dtype, state, need, layout = _head_scan_fwd_plan(
+        *_meta(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, Dskip=Dskip, dt_bias=dt_bias, y=y, h0=h0, hL=hL, cu_seqlens=cu_seqlens,
+               workspace=ws), out_dtype)
+    dev = x.device
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    if hL is None and return_final_state:
+        hL = torch.empty(state, dtype=torch.float32, device=dev)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().ssm_head_scan_fwd(
+        *sizes[:6], code, SSM_FLAG_CHECKPOINTS if checkpoints is not None else 0, x.data_ptr(), dt.data_ptr(),
+        _at(dt_bias), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _at(Dskip), _at(h0), _at(cu_seqlens), sizes[6],
+        out_code, y.data_ptr(), _at(hL), _at(ws), _bytes(ws), layout, _stream(stream, dev)))
+    return y, hL
+
+
+@_on_caller_stream
+def ssm_head_scan_bwd(x, dt, A, Bm, Cm, dy, *, Dskip=None, dt_bias=None, h0=None, dhL=None, cu_seqlens=None,
+                      workspace=None, checkpoints_in_workspace=False, dx=None, ddt=None, dBm=None, dCm=None,
+                      stream=None):
+    """Gradients of ssm_head_scan_fwd; returns a dict with dx, ddt, dBm, dCm
+    (dy's dtype), dA, dDskip, ddt_bias (None where Dskip or dt_bias is not
+    given) and dh0 (fp32).  workspace: from ssm_head_scan_bwd_workspace
+    (allocated here when not given); checkpoints_in_workspace=True when
+    ssm_head_scan_fwd filled it for the same inputs."""
+    sizes, code, g_code, state, layout = _head_scan_bwd_plan(
+        *_meta(x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, dy=dy, Dskip=Dskip, dt_bias=dt_bias, h0=h0, dhL=dhL,
+               cu_seqlens=cu_seqlens, workspace=workspace, dx=dx, ddt=ddt, dBm=dBm, dCm=dCm))
+    if workspace is None:
+        if checkpoints_in_workspace:
+            raise ValueError("checkpoints_in_workspace needs the workspace that ssm_head_scan_fwd filled")
+        workspace = ssm_head_scan_bwd_workspace(x, Bm, cu_seqlens=cu_seqlens)
+    gt, dev, f32 = dy.dtype, x.device, torch.float32
+    new = lambda given, shape: torch.empty(shape, dtype=gt, device=dev) if given is None else given  # noqa: E731
+    head = lambda: torch.empty(sizes[3], dtype=f32, device=dev)  # noqa: E731
+    out = {"dx": new(dx, x.shape), "ddt": new(ddt, dt.shape), "ddt_bias": head() if dt_bias is not None else None,
+           "dA": head(), "dBm": new(dBm, Bm.shape), "dCm": new(dCm, Bm.shape),
+           "dDskip": head() if Dskip is not None else None, "dh0": torch.empty(state, dtype=f32, device=dev)}
+    _check(lib().ssm_head_scan_bwd(
+        *sizes[:6], code, SSM_FLAG_CHECKPOINTS if checkpoints_in_workspace else 0, x.data_ptr(), dt.data_ptr(),
+        _at(dt_bias), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _at(Dskip), _at(h0), _at(cu_seqlens), sizes[6],
+        g_code, dy.data_ptr(), _at(dhL), *[_at(t) for t in out.values()], workspace.data_ptr(), _bytes(workspace),
+        layout, _stream(stream, dev)))
+    return out
+
+
+@_on_caller_stream
+def ssm_head_scan_update(state, x, dt, A, Bm, Cm, *, Dskip=None, dt_bias=None, slots=None, out_dtype=None, y=None,
+                         stream=None):
+    """One decode step of the head scan; updates `state` [slots, heads, N, P]
+    (fp32) in place and returns y [batch, heads, P].  x [batch, heads, P], dt
+    [batch, heads], Bm and Cm [batch, groups, N].  slots: int32 device tensor
+    with each row's state (None: row b uses state b; a negative or too large
+    slot skips the row, its y is zero)."""
+    sizes, num_slots, out_code, out_dtype, shape, layout = _head_scan_update_plan(
+        *_meta(state=state, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, Dskip=Dskip, dt_bias=dt_bias, y=y, slots=slots), out_dtype)
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype, device=x.device)
+    _check(lib().ssm_head_scan_update(
+        *sizes, state.data_ptr(), num_slots, _at(slots), x.data_ptr(), dt.data_ptr(), _at(dt_bias), A.data_ptr(),
+        Bm.data_ptr(), Cm.data_ptr(), _at(Dskip), out_code, y.data_ptr(), layout, _stream(stream, x.device)))
+    return y
+
+
+def _rms_code(t):
+    return SSM_E4M3 if t == torch.float8_e4m3fn else _dtype_code(t)
+
+
+_BT = ("batch", "step")
+
+
+@_plan
+def _rms_fwd_plan(x, residual, residual_out, y, scales, weight, out_dtype, stream_dtype):
+    every = (x, residual, residual_out, y, scales, weight)
+    _whole(*every)
+    if len(x[1]) not in (2, 3):
+        raise ValueError("x must be [batch, L, dim] or [batch, dim]")
+    shape, order = x[1], _BT[:len(x[1]) - 1]
+    ind = x[3]
+    out_dtype = y[3] if y is not None else out_dtype or ind
+    kept = residual if residual is not None else residual_out
+    stream_dtype = kept[3] if kept is not None else stream_dtype
+    layout = _layout(RmsLayout, order, (x, shape, ind), (residual, shape, stream_dtype),
+                     (residual_out, shape, stream_dtype), (y, shape, out_dtype))
+    blocks = tuple(shape[:-1]) + (-(-shape[-1] // 128),)
+    if out_dtype == torch.float8_e4m3fn:
+        if scales is not None:
+            _expect(scales, blocks, torch.float32)
+            for d, name in enumerate(["scale_" + n for n in order] + ["scale_block"]):
+                setattr(layout, name, scales[2][d] if blocks[d] > 1 else 0)
+    elif scales is not None:
+        raise ValueError("scales are the output of out_dtype torch.float8_e4m3fn only")
+    _dense((weight, (shape[-1],), torch.float32))
+    _on_gpu(*every)
+    sizes = (shape[0], shape[1] if len(shape) == 3 else 1, shape[-1])
+    code = _dtype_code(stream_dtype) if stream_dtype is not None else SSM_F32
+    return (sizes, _dtype_code(ind), code, stream_dtype, _rms_code(out_dtype), out_dtype, blocks, ctypes.byref(layout))
+
+
+@_on_caller_stream
+def ssm_rms_norm_fwd(x, *, weight=None, residual=None, eps=None, out_dtype=None, stream_dtype=None,
+                     residual_out=None, y=None, scales=None, stream=None):
+    """h = x + residual and y = h / sqrt(mean(h^2) + eps) * weight over the last
+    index of [batch, L, dim] or [batch, dim] tensors (channels contiguous, step
+    and batch strides free); returns (y, h, scales).  h has residual's dtype,
+    or stream_dtype where there is no residual (None: h is x, and None is
+    returned in its place).  weight [dim] fp32; out_dtype defaults to x's.  With
+    out_dtype torch.float8_e4m3fn, y comes in 8 bits and scales [.., ceil(dim /
+    128)] fp32 holds a scale for every 128 channels (y is about y.float() *
+    scale); otherwise scales is None.  residual_out may be residual (the stream
+    moves on in place)."""
+    (sizes, code, s_code, stream_dtype, out_code, out_dtype, blocks, layout) = _rms_fwd_plan(
+        *_meta(x=x, residual=residual, residual_out=residual_out, y=y, scales=scales, weight=weight), out_dtype,
+        stream_dtype)
+    dev = x.device
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    if residual_out is None and stream_dtype is not None:
+        residual_out = torch.empty(x.shape, dtype=stream_dtype, device=dev)
+    if scales is None and out_code == SSM_E4M3:
+        scales = torch.empty(blocks, dtype=torch.float32, device=dev)
+    _check(lib().ssm_rms_norm_fwd(
+        *sizes, code, s_code, _float(eps), x.data_ptr(), _at(residual), _at(weight), _at(residual_out), out_code,
+        y.data_ptr(), _at(scales), layout, _stream(stream, dev)))
+    return y, residual_out, scales
+
+
+@_plan
+def _rms_bwd_plan(h, dy, dh, dx, dresidual, weight, workspace):
+    every = (h, dy, dh, dx, dresidual, weight, workspace)
+    _whole(*every)
+    if len(h[1]) not in (2, 3):
+        raise ValueError("h must be [batch, L, dim] or [batch, dim]")
+    shape, st, gt = h[1], h[3], dy[3]
+    layout = _layout(RmsBwdLayout, _BT[:len(shape) - 1], (h, shape, st), (dy, shape, gt), (dh, shape, st),
+                     (dx, shape, gt), (dresidual, shape, st))
+    _dense((weight, (shape[-1],), torch.float32), (workspace, None, None))
+    _on_gpu(*every)
+    sizes = (shape[0], shape[1] if len(shape) == 3 else 1, shape[-1])
+    return (sizes, _dtype_code(st), _dtype_code(gt), max(1, lib().ssm_rms_norm_bwd_workspace_bytes(*sizes)),
+            ctypes.byref(layout))
+
+
+@_on_caller_stream
+def ssm_rms_norm_bwd(h, dy, *, weight=None, dh=None, eps=None, residual=None, dx=None, dresidual=None,
+                     workspace=None, stream=None):
+    """Gradients of ssm_rms_norm_fwd; h is what it returned (or its x, where it
+    returned None), dh the gradient that comes down the residual stream.
+    Returns a dict with dx (dy's dtype), dresidual (h's dtype; the same tensor
+    as dx where the types agree and neither is given; None unless residual,
+    which defaults to whether dh is given) and dweight (fp32; None without
+    weight)."""
+    sizes, s_code, g_code, need, layout = _rms_bwd_plan(
+        *_meta(h=h, dy=dy, dh=dh, dx=dx, dresidual=dresidual, weight=weight, workspace=workspace))
+    dev = h.device
+    if residual is None:
+        residual = dh is not None
+    same = residual and dresidual is None and dx is None and h.dtype == dy.dtype
+    if residual and dresidual is None and not same:
+        dresidual = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    if dx is None:
+        dx = torch.empty(h.shape, dtype=dy.dtype, device=dev)
+    dw = None
+    if weight is not None:
+        dw = torch.empty(sizes[2], dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib().ssm_rms_norm_bwd(
+        *sizes, s_code, g_code, _float(eps), h.data_ptr(), _at(weight), dy.data_ptr(), _at(dh), dx.data_ptr(),
+        _at(dresidual), _at(dw), _at(workspace), _bytes(workspace), layout, _stream(stream, dev)))
+    return {"dx": dx, "dresidual": dx if same else dresidual, "dweight": dw}
+
+
 scan_fwd = ssm_scan_fwd
 scan_bwd = ssm_scan_bwd
 scan_bwd_bld = ssm_scan_bwd_bld
@@ -1107,3 +1414,8 @@ delta_bwd = ssm_delta_bwd
 delta_update = ssm_delta_update
 group_norm_fwd = ssm_group_norm_fwd
 group_norm_bwd = ssm_group_norm_bwd
+head_scan_fwd = ssm_head_scan_fwd
+head_scan_bwd = ssm_head_scan_bwd
+head_scan_update = ssm_head_scan_update
+rms_norm_fwd = ssm_rms_norm_fwd
+rms_norm_bwd = ssm_rms_norm_bwd

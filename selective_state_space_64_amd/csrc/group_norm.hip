@@ -491,21 +491,6 @@ bool norm_sizes(int batch, int seqlen, int dim, int groups)
            (long long)batch * seqlen < (1ll << 31);
 }
 
-// Strides with defaults filled in and the span in elements; false when below
-// the dense minimum or spanning 2^56 elements.
-bool norm_strides(long long given_step, long long given_batch, int batch, int seqlen, int dim,
-                  long long &st, long long &sb, size_t &sp)
-{
-    st = given_step ? given_step : dim;
-    if (st < dim || st > (1ll << 40)) return false;
-    sb = given_batch ? given_batch : seqlen * st;
-    if ((__int128)sb < (__int128)seqlen * st) return false;
-    const __int128 n = (__int128)(batch - 1) * sb + (__int128)(seqlen - 1) * st + dim;
-    if (n >= ((__int128)1 << 56)) return false;
-    sp = size_t(n);
-    return true;
-}
-
 // Tensor i for the overlap check; the batch stride of one entry leads nowhere.
 Steps norm_steps(const void *ptr, size_t span, size_t es, const NormParams &p, int i, int batch, int seqlen, int dim)
 {
@@ -561,7 +546,7 @@ ssm_status_t ssm_group_norm_fwd(int batch, int seqlen, int dim, int groups, ssm_
     size_t sp[3];
     const int at[3] = {0, 1, 3};
     for (int i = 0; i < 3; ++i)
-        if (!norm_strides(lay.step[i], lay.batch[i], batch, seqlen, dim, p.step[at[i]], p.batch[at[i]], sp[i]))
+        if (!row_strides(lay.step[i], lay.batch[i], batch, seqlen, dim, p.step[at[i]], p.batch[at[i]], sp[i]))
             return SSM_ERR_BAD_SHAPE;
     const size_t es = dsize(in_t), os = dsize(out_t);
     if (misaligned(x, es) || misaligned(z, es) || misaligned(y, os) || misaligned(weight, 4) ||
@@ -625,7 +610,7 @@ ssm_status_t ssm_group_norm_bwd(int batch, int seqlen, int dim, int groups, ssm_
     NormParams p{};
     size_t sp[5];
     for (int i = 0; i < 5; ++i)
-        if (!norm_strides(lay.step[i], lay.batch[i], batch, seqlen, dim, p.step[i], p.batch[i], sp[i]))
+        if (!row_strides(lay.step[i], lay.batch[i], batch, seqlen, dim, p.step[i], p.batch[i], sp[i]))
             return SSM_ERR_BAD_SHAPE;
     const size_t es = dsize(in_t), gs = dsize(g_t), wb = 4 * size_t(dim);
     const void *ptrs[5] = {x, z, dy, dx, dz};

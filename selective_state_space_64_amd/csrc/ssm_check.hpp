@@ -61,6 +61,21 @@ inline bool overlaps(const Steps &a, const Steps &b)
     return d < a.run || d + b.run > step;
 }
 
+// Strides of a [batch][seqlen][dim] tensor with defaults filled in and the span
+// in elements; false when below the dense minimum or spanning 2^56 elements.
+inline bool row_strides(long long given_step, long long given_batch, int batch, int seqlen, int dim,
+                        long long &st, long long &sb, size_t &sp)
+{
+    st = given_step ? given_step : dim;
+    if (st < dim || st > (1ll << 40)) return false;
+    sb = given_batch ? given_batch : seqlen * st;
+    if ((__int128)sb < (__int128)seqlen * st) return false;
+    const __int128 n = (__int128)(batch - 1) * sb + (__int128)(seqlen - 1) * st + dim;
+    if (n >= ((__int128)1 << 56)) return false;
+    sp = size_t(n);
+    return true;
+}
+
 // The value of an enum argument as the int a C caller passed: its bits are
 // read without loading the argument as the enum type, so a value outside the
 // enumeration (an error the validation reports) is not undefined behaviour.
