@@ -138,55 +138,110 @@ __device__ inline void to_floats(const F32x8 &v, f32x4 &lo, f32x4 &hi)
     hi = v.hi;
 }
 
+// Hides where a value comes from, so that what is computed of it in a loop is
+// not kept in registers from before the loop.
+__device__ inline void opaque(uint32_t &v) { asm volatile("" : "+v"(v)); }
+
+// An operand is formed here and not later: the compiler moves what has no side
+// effects to where it is used, out of the shadow of the matrix instructions that
+// stand beside it in the source.
+template <int N> __device__ inline void pin(Frag<N> &f)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f.t[i]));
+}
+__device__ inline void pin(F32x8 &) {}
+
 // 64 rows on their way from memory to a tile.  kFast: in registers from
-// fetch() to store(), 16-byte loads; otherwise store() loads them element by
-// element, of the type that `bf16` says (fp32 compute takes either).
+// fetch() to store(), 16-byte loads from one buffer whose end stands for the
+// masks of rows; otherwise store() loads them element by element, of the type
+// that `bf16` says (fp32 compute takes either).
 template <typename T, int NCH, bool kFast> struct TileIn {
-    static constexpr int kPer = 64 * NCH / kThreads;
-    TileLoad<T, NCH, kThreads, true> load;
+    static constexpr int kPer = 64 * NCH / kThreads, kWords = int(sizeof(T) / 2);
+    u32x4 raw[kFast ? kPer : 1][kWords];
+    uint32_t off, run;  // of the thread's first chunk; from one of its rows to the next
+    // rows `step` elements apart, columns [0, n) exist
     __device__ inline void init(long long step, int n)
     {
-        if constexpr (kFast) load.init(step, n);
+        if constexpr (kFast) {
+            const int t = int(threadIdx.x) / NCH, c = int(threadIdx.x) % NCH;
+            run = uint32_t(kThreads / NCH) * uint32_t(step) * uint32_t(sizeof(T));
+            off = c * 8 < n ? uint32_t(t * int(step) + c * 8) * uint32_t(sizeof(T)) : kOutside;
+        }
     }
-    // rows >= 1 from p on, columns [0, n) exist
-    __device__ inline void fetch(const void *p, long long step, int rows, int n)
+    // rows >= 1 from p on
+    __device__ inline void fetch(const void *p, long long step, int rows)
     {
-        if constexpr (kFast) load.fetch(static_cast<const T *>(p), step, rows, n);
+        if constexpr (kFast) {
+            const auto buf = buffer_of(p, (long long)(rows * int(step)) * int(sizeof(T)));
+            uint32_t off = this->off;
+            opaque(off);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    raw[i][w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off + i * run + 16 * w, 0, 0));
+        }
     }
     __device__ inline void store(E<T> *tile, const void *p, long long step, int rows, int n, int bf16) const
     {
         if constexpr (kFast) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) put(tile, i, load.raw[i]);
+            for (int i = 0; i < kPer; ++i) put(tile, i, raw[i]);
         } else {
             for (int i = 0; i < kPer; ++i) {
                 const int at = int(threadIdx.x) + i * kThreads, t = at / NCH, c = at % NCH;
                 const long long row = (long long)min(t, rows - 1) * step;
                 const int count = t < rows ? n - c * 8 : 0;
-                if constexpr (sizeof(T) == 2) {
-                    put(tile, i, n < 1 ? Raw8<T>{} : keep8(load8(static_cast<const T *>(p) + row, c, n), count));
-                } else if (!bf16) {
-                    put(tile, i, n < 1 ? Raw8<T>{} : keep8(load8(static_cast<const T *>(p) + row, c, n), count));
+                if (sizeof(T) == 2 || !bf16) {
+                    put(tile, i, (n < 1 ? Raw8<T>{} : keep8(load8(static_cast<const T *>(p) + row, c, n), count)).w);
                 } else {
                     const Raw8<bf16_t> v =
                         n < 1 ? Raw8<bf16_t>{} : keep8(load8(static_cast<const bf16_t *>(p) + row, c, n), count);
                     f32x4 lo, hi;
                     to_floats(__builtin_bit_cast(bf16x8, v.w[0]), lo, hi);
-                    put(tile, i, Raw8<T>{{__builtin_bit_cast(u32x4, lo), __builtin_bit_cast(u32x4, hi)}});
+                    const u32x4 w[2] = {__builtin_bit_cast(u32x4, lo), __builtin_bit_cast(u32x4, hi)};
+                    put(tile, i, w);
                 }
             }
         }
     }
-    __device__ static inline void put(E<T> *tile, int i, const Raw8<T> &v)
+    __device__ static inline void put(E<T> *tile, int i, const u32x4 *w)
     {
         const int at = int(threadIdx.x) + i * kThreads;
         u32x4 *to = reinterpret_cast<u32x4 *>(tile + chunk_at<NCH>(at / NCH, at % NCH));
 #pragma unroll
-        for (int w = 0; w < int(sizeof(T) / 2); ++w) to[w] = v.w[w];
+        for (int k = 0; k < kWords; ++k) to[k] = w[k];
     }
 };
 
 // ---------------------------------------------------------------- a chunk's decays
+// Sums over the lanes up to each one, in double: inside 16 lanes by shifts, then
+// the last lane of a row to the row behind it and of the first half to the second.
+template <int kCtrl, int kRows> __device__ inline double dpp_add(double v)
+{
+    const unsigned long long bits = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = unsigned(__builtin_amdgcn_update_dpp(0, int(unsigned(bits)), kCtrl, kRows, 0xf, false));
+    const unsigned hi = unsigned(__builtin_amdgcn_update_dpp(0, int(unsigned(bits >> 32)), kCtrl, kRows, 0xf, false));
+    return v + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ inline double wave_prefix(double v)
+{
+    v = dpp_add<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8 (lanes without a source add 0)
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);         // row_bcast 15, to rows 1 and 3
+    return dpp_add<0x143, 0xc>(v);      // row_bcast 31, to rows 2 and 3
+}
+__device__ inline double from_lane(double v, int lane)
+{
+    const unsigned long long bits = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = unsigned(__builtin_amdgcn_readlane(int(unsigned(bits)), lane));
+    const unsigned hi = unsigned(__builtin_amdgcn_readlane(int(unsigned(bits >> 32)), lane));
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+
 // Lane t of a wave has step t; G in units of log2.
 struct Decays {
     float dt;    // softplus(dt + bias), 0 behind the last row
@@ -203,13 +258,8 @@ __device__ inline Decays decays(float raw, float bias, float A, int rows)
     // a decay of e^-110 is 0 in fp32; clamped, it does not cost later steps'
     // differences their low bits (a NaN stays one)
     const double a = double(d.dt) * double(A);
-    d.G = live ? (a < -110.0 ? -110.0 : a) * 1.4426950408889634 : 0.0;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const double before = __shfl_up(d.G, o);
-        if (int(threadIdx.x & 63) >= o) d.G += before;
-    }
-    d.end = __shfl(d.G, 63);
+    d.G = wave_prefix(live ? (a < -110.0 ? -110.0 : a) * 1.4426950408889634 : 0.0);
+    d.end = from_lane(d.G, 63);
     return d;
 }
 // 2^v for v of any size, to about an ulp: the fraction that float(v) loses is put back.
@@ -219,6 +269,12 @@ __device__ inline float exp2_of(double v)
     const float lo = float(v - double(hi));
     return exp2_hw(hi) * __builtin_fmaf(lo, kLn2, 1.0f);
 }
+// A chunk's decays for a workgroup: G as two floats, the step size, the scales
+// of rows that read the state and of rows that enter it, e^{Gc}.
+struct Vec {
+    float hi[64], lo[64], dt[64], out[64], in[64], end[4];
+};
+
 // Element loads of a [steps] column of either type.
 __device__ inline float load_step(const void *p, long long at, int bf16)
 {

@@ -96,8 +96,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
         TileIn<T, NCH, kFast> inB, inC;
         inB.init(p.sB.t, p.N);
         inC.init(p.sC.t, p.N);
-        inB.fetch(in_at(p.B, p.sB, group, ein), p.sB.t, rows, p.N);
-        inC.fetch(in_at(p.C, p.sC, group, ein), p.sC.t, rows, p.N);
+        inB.fetch(in_at(p.B, p.sB, group, ein), p.sB.t, rows);
+        inC.fetch(in_at(p.C, p.sC, group, ein), p.sC.t, rows);
         inB.store(tB, in_at(p.B, p.sB, group, ein), p.sB.t, rows, p.N, p.in_bf16);
         inC.store(tC, in_at(p.C, p.sC, group, ein), p.sC.t, rows, p.N, p.in_bf16);
     }
@@ -108,8 +108,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     auto fetch = [&](int k, int pb) {
         inX.init(p.sx.t, p.P - pb * PB);
         inY.init(p.sdy.t, p.P - pb * PB);
-        inX.fetch(x_at(k, pb), p.sx.t, rows, p.P - pb * PB);
-        inY.fetch(y_at(k, pb), p.sdy.t, rows, p.P - pb * PB);
+        inX.fetch(x_at(k, pb), p.sx.t, rows);
+        inY.fetch(y_at(k, pb), p.sdy.t, rows);
     };
     fetch(0, 0);
     __syncthreads();

@@ -28,11 +28,39 @@ namespace {
 // every chunk; only these; or a segment's end state and decay.
 enum { kOutRun = 0, kOutKeepRun = 1, kKeepRun = 2, kEndRun = 3 };
 
-// A chunk's decays for the workgroup: G as two floats, D, the scales of rows
-// that read the state (out) and of rows that enter it (in), e^{Gc}.
-struct Vec {
-    float hi[64], lo[64], dt[64], out[64], in[64], end[4];
-};
+// Rows 16 m + r, columns c .. c + 3 of y[m], `rows` and `cols` of them there.  kFast: the
+// columns are stored together, into one buffer whose end stands for the mask of rows.
+template <bool kFast>
+__device__ inline void store_out(char *out, long long step, int bf16, int rows, int c, int cols, int r, const f32x4 *y)
+{
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    if constexpr (kFast) {
+        const int row = int(step) * (bf16 ? 2 : 4);
+        const auto buf = buffer_of(out, rows * (long long)row);
+        const uint32_t off = c < cols ? uint32_t(r * row + c * (bf16 ? 2 : 4)) : kOutside;
+        if (bf16) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(y[m][0], y[m][1]), pack_bf16x2(y[m][2], y[m][3])},
+                                                      buf, off + uint32_t(16 * m * row), 0, 0);
+        } else {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[m]), buf, off + uint32_t(16 * m * row), 0, 0);
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const long long at = (long long)(16 * m + r) * step + c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (16 * m + r < rows && c + e < cols) {
+                    if (bf16) reinterpret_cast<bf16_t *>(out)[at + e].bits = uint16_t(pack_bf16x2(y[m][e], y[m][e]));
+                    else reinterpret_cast<float *>(out)[at + e] = y[m][e];
+                }
+        }
+    }
+}
 
 template <typename T, int ND, int kRun, bool kRev, bool kFast>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) void heads_scan_kernel(const HeadsScan p)
@@ -44,12 +72,15 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     // value, under the rounding of a bf16 y); what enters the state: three (2^-25),
     // since the fp32 states of a whole sequence are sums of it.
     constexpr int NW = 2, NR = 2, NX = 3;
-    constexpr int kTri = kTriFrags * 512 * (sizeof(T) == 2 ? NW : 1);
+    constexpr int kFrag = 512 * (sizeof(T) == 2 ? NW : 1);
+    // Chunks whose decays are formed at a time, a wave each; the next ones' while these
+    // are in work (fp32 tiles of 256 entries leave LDS for two).
+    constexpr int kAhead = sizeof(T) == 4 && ND == 256 ? 1 : kWaves;
     __shared__ __align__(16) E<T> tileL[kOut ? kTile : 8];
     __shared__ __align__(16) E<T> tileR[kTile];
     __shared__ __align__(16) E<T> tileV[64 * kCols];
-    __shared__ __align__(16) E<T> tri[kOut ? kTri : 8];
-    __shared__ __align__(16) Vec vecs[2];
+    __shared__ __align__(16) E<T> tri[kOut ? kTriFrags * kFrag : 8];
+    __shared__ __align__(16) Vec vecs[2 * kAhead];
 
     const int head = int(blockIdx.y), group = head / p.rep, l = int(threadIdx.x) & 63, wave = wave_of();
     const int r = l & 15, g = l >> 4;
@@ -65,27 +96,20 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     const long long state_at = ((long long)seg.seq * p.h + head) * p.N * (long long)p.P + col;
     const long long slot = (long long)blockIdx.x * p.h + head;
     // this segment's place in ends, the one before it in the run's order, and the last one's
-    float *const end_to = p.ws.ends + slot * p.ws.state + col;
+    float *const end_to = p.ws.ends + slot * p.ws.state;
     const float *const entry = p.ws.ends + (slot + (kRev ? p.h : -p.h)) * p.ws.state + col;
-    float *const initial = p.ws.ends + (slot + (long long)p.h * (kRev ? -seg.index : seg.behind)) * p.ws.state + col;
+    float *const initial = p.ws.ends + (slot + (long long)p.h * (kRev ? -seg.index : seg.behind)) * p.ws.state;
     const bool split = p.ws.seg_chunks > 0 && !(first && last);
-
-    const char *const L0 = static_cast<const char *>(p.L), *const R0 = static_cast<const char *>(p.R);
-    const int ein = p.in_bf16 ? 2 : 4, ev = p.v_bf16 ? 2 : 4;
-    const long long l_at = seq.batch * p.sL_.b + seq.first * p.sL_.t + group * p.sL_.h;
-    const long long r_at = seq.batch * p.sR.b + seq.first * p.sR.t + group * p.sR.h;
-    const long long v_at = seq.batch * p.sv.b + seq.first * p.sv.t + head * p.sv.h + col0;
-    const long long dt_at = seq.batch * p.sdt.b + seq.first * p.sdt.t + head * p.sdt.h;
-    const long long out_at = seq.batch * p.sout.b + seq.first * p.sout.t + head * p.sout.h;
     const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.0f, D = p.D ? p.D[head] : 0.0f;
 
     // S: tiles 2 b and 2 b + 1 hold the rows 32 b + 8 g + {0..3} and + {4..7}
     f32x4 S[ND / 16];
+    auto row_of = [&](int m, int e) { return 32 * (m / 2) + 8 * g + 4 * (m % 2) + e; };
 #pragma unroll
     for (int m = 0; m < ND / 16; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
+            const int row = row_of(m, e);
             float s = 0.0f;
             if (!first) {
                 if (!kEnd && kept && row < p.ws.Nr) s = entry[(long long)row * p.ws.Pp];
@@ -93,45 +117,71 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
                 // a split sequence's initial state: kept by the ends' run, because sL may
                 // be the same memory and the last segment may end before the first begins
                 if (split && !kEnd) {
-                    if (kept && row < p.ws.Nr) s = initial[(long long)row * p.ws.Pp];
+                    if (kept && row < p.ws.Nr) s = initial[(long long)row * p.ws.Pp + col];
                 } else if (mine && row < p.N) {
                     s = p.s0[state_at + (long long)row * p.P];
                 }
             }
             S[m][e] = s;
         }
+    // rows behind Nr lie behind the record's end and are not stored
+    const uint32_t keep_off = kept ? uint32_t(8 * g * p.ws.Pp + col) * 4u : kOutside;
     auto keep_state = [&](float *to) {
-        if (kept) {
+        const auto buf = buffer_of(to, p.ws.state * 4);
+        uint32_t off = keep_off;
+        opaque(off);
 #pragma unroll
-            for (int m = 0; m < ND / 16; ++m)
+        for (int m = 0; m < ND / 16; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
-                    if (row < p.ws.Nr) to[(long long)row * p.ws.Pp] = S[m][e];
-                }
-        }
+            for (int e = 0; e < 4; ++e)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][e]), buf,
+                                                      off + uint32_t((32 * (m / 2) + 4 * (m % 2) + e) * p.ws.Pp) * 4u, 0, 0);
     };
     if (kEnd && first && p.s0) keep_state(initial);
 
+    // the chunks in the order of the run, and where each one's rows begin
+    const int ein = p.in_bf16 ? 2 : 4, ev = p.v_bf16 ? 2 : 4, eo = p.out_bf16 ? 2 : 4;
     auto chunk_of = [&](int k) { return kRev ? seg.c1 - 1 - k : c0 + k; };
+    const long long begin = seq.first + (long long)chunk_of(0) * kDeltaChunk;
+    const int turn = kRev ? -kDeltaChunk : kDeltaChunk;
+    const char *pL = static_cast<const char *>(p.L) + (seq.batch * p.sL_.b + begin * p.sL_.t + group * p.sL_.h) * ein;
+    const char *pR = static_cast<const char *>(p.R) + (seq.batch * p.sR.b + begin * p.sR.t + group * p.sR.h) * ein;
+    const char *pV = static_cast<const char *>(p.v) + (seq.batch * p.sv.b + begin * p.sv.t + head * p.sv.h + col0) * ev;
+    char *pO = static_cast<char *>(p.out) + (seq.batch * p.sout.b + begin * p.sout.t + head * p.sout.h + col0) * eo;
+    const long long dL = turn * p.sL_.t * ein, dR = turn * p.sR.t * ein, dV = turn * p.sv.t * ev, dO = turn * p.sout.t * eo;
+    float *pK = p.keep + (((long long)seq.chunk0 + chunk_of(0)) * p.h + head) * p.ws.state;
+    const long long dK = (kRev ? -p.h : p.h) * p.ws.state;
+    const long long dt_at = seq.batch * p.sdt.b + seq.first * p.sdt.t + head * p.sdt.h;
+
     TileIn<T, NCH, kFast> inL, inR;
     TileIn<T, kVCH, kFast> inV;
     inL.init(p.sL_.t, p.N);
     inR.init(p.sR.t, p.N);
     inV.init(p.sv.t, p.P - col0);
-    float raw = 0.0f;
-    auto fetch = [&](int c) {
-        const long long t = (long long)c * kDeltaChunk;
-        const int rows = min(seq.len - c * kDeltaChunk, kDeltaChunk);
-        if constexpr (kOut) inL.fetch(L0 + (l_at + t * p.sL_.t) * ein, p.sL_.t, rows, p.N);
-        inR.fetch(R0 + (r_at + t * p.sR.t) * ein, p.sR.t, rows, p.N);
-        inV.fetch(static_cast<const char *>(p.v) + (v_at + t * p.sv.t) * ev, p.sv.t, rows, p.P - col0);
-        if (wave == kWaves - 1) raw = load_step(p.dt, dt_at + (t + min(l, rows - 1)) * p.sdt.t, p.in_bf16);
+    auto rows_of = [&](int k) { return min(seq.len - chunk_of(k) * kDeltaChunk, kDeltaChunk); };
+    auto fetch = [&](const char *l_at, const char *r_at, const char *v_at, int rows) {
+        if constexpr (kOut) inL.fetch(l_at, p.sL_.t, rows);
+        inR.fetch(r_at, p.sR.t, rows);
+        inV.fetch(v_at, p.sv.t, rows);
     };
-    double passed = 0.0;  // the segment's decay
-    auto prepare = [&](int c, Vec &v) {
-        if (wave != kWaves - 1) return;
-        const Decays d = decays(raw, bias, A, min(seq.len - c * kDeltaChunk, kDeltaChunk));
+    auto store = [&](int k) {
+        const int rows = rows_of(k);
+        if constexpr (kOut) inL.store(tileL, pL, p.sL_.t, rows, p.N, p.in_bf16);
+        inR.store(tileR, pR, p.sR.t, rows, p.N, p.in_bf16);
+        inV.store(tileV, pV, p.sv.t, rows, p.P - col0, p.v_bf16);
+    };
+    // the wave's chunk of those from `base` on
+    float raw = 0.0f;
+    auto load_raw = [&](int base) {
+        if (wave < kAhead && base + wave < n)
+            raw = load_step(p.dt, dt_at + ((long long)chunk_of(base + wave) * kDeltaChunk + min(l, rows_of(base + wave) - 1)) * p.sdt.t,
+                            p.in_bf16);
+    };
+    double passed = 0.0;  // the wave's part of the segment's decay
+    auto prepare = [&](int base) {
+        if (wave >= kAhead || base + wave >= n) return;
+        const Decays d = decays(raw, bias, A, rows_of(base + wave));
+        Vec &v = vecs[(base + wave) & (2 * kAhead - 1)];
         v.hi[l] = float(d.G);
         v.lo[l] = float(d.G - double(float(d.G)));
         v.dt[l] = d.dt;
@@ -143,100 +193,195 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     };
 
     if (n > 0) {
-        fetch(chunk_of(0));
-        prepare(chunk_of(0), vecs[0]);
-    }
-    for (int k = 0; k < n; ++k) {
-        const int c = chunk_of(k), rows = seq.len - c * kDeltaChunk;
-        const long long t = (long long)c * kDeltaChunk;
-        const Vec &vec = vecs[k & 1];
-        __syncthreads();  // the last chunk's reads are done
-        {
-            const int have = min(rows, kDeltaChunk);
-            if constexpr (kOut) inL.store(tileL, L0 + (l_at + t * p.sL_.t) * ein, p.sL_.t, have, p.N, p.in_bf16);
-            inR.store(tileR, R0 + (r_at + t * p.sR.t) * ein, p.sR.t, have, p.N, p.in_bf16);
-            inV.store(tileV, static_cast<const char *>(p.v) + (v_at + t * p.sv.t) * ev, p.sv.t, have, p.P - col0,
-                      p.v_bf16);
-        }
+        load_raw(0);
+        fetch(pL, pR, pV, rows_of(0));
+        if constexpr (kOut)  // the halves of fragments on the far side of the diagonal stay 0
+            for (int i = int(threadIdx.x); i < kTriFrags * kFrag; i += kThreads) tri[i] = E<T>(0);
+        prepare(0);
+        load_raw(kAhead);
+        store(0);
         __syncthreads();
-        if (k + 1 < n) fetch(chunk_of(k + 1));
-        if constexpr (kKeep) {
-            const long long record = (long long)seq.chunk0 + c;
-            keep_state(p.keep + (record * p.h + head) * p.ws.state + col);
+    }
+    // Two barriers a chunk: all that reads the tiles stands before the first, where W is
+    // complete too; the next chunk's tiles are stored behind it, beside W v.  Between them
+    // each phase's fragments are read while the phase before it computes, and the vector
+    // work (terms, decays) takes turns with matrix instructions that do not wait for it.
+    for (int k = 0; k < n; ++k) {
+        const Vec &vec = vecs[k & (2 * kAhead - 1)];
+        if ((k & (kAhead - 1)) == 0) {
+            prepare(k + kAhead);
+            load_raw(k + 2 * kAhead);
         }
-        // W's column tile of this wave (rows of R 16 wave ..), and S^T L
-        f32x4 y[4];
-        if constexpr (kOut) {
-            f32x4 w[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) y[m] = w[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                In<T> fl[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) fl[m] = tile_row<T, NCH>(tileL, 16 * m + r, 4 * b + g);
-                const In<T> fr = tile_row<T, NCH>(tileR, 16 * wave + r, 4 * b + g);
-                mma_right<4>(w, fr, fl);
-                mma_left<4>(y, fl, to_sum<T, NR>(S[2 * b], S[2 * b + 1]));
-            }
-            // w[m]: rows of R 16 wave + 4 g + e, row of L 16 m + r
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(vec.hi + 16 * wave + 4 * g);
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(vec.lo + 16 * wave + 4 * g);
-            const f32x4 dts = *reinterpret_cast<const f32x4 *>(vec.dt + 16 * wave + 4 * g);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int i = 16 * m + r;
-                const float ihi = vec.hi[i], ilo = vec.lo[i], idt = vec.dt[i];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * wave + 4 * g + e;
-                    const float d = (ihi - hi[e]) + (ilo - lo[e]);
-                    const float f = exp2_hw(kRev ? -d : d) * (kRev ? idt : dts[e]);
-                    w[m][e] = (kRev ? j >= i : j <= i) ? w[m][e] * f : 0.0f;
-                }
-                // the half of a fragment that these four are, if the triangle has it
-                const int block = wave >> 1;
-                if (kRev ? m < 2 || block == 1 : m >= 2 || block == 0) {
-                    E<T> *to = tri + (kRev ? tri_upper(m, block) : tri_lower(m, block)) * (kTri / kTriFrags);
-                    if constexpr (sizeof(T) == 4) {
-                        *reinterpret_cast<f32x4 *>(to + l * 8 + 4 * (wave & 1)) = w[m];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NW; ++i) {
-                            typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-                            float a = w[m][0], b = w[m][1], c2 = w[m][2], d2 = w[m][3];
-                            const u32x2 bits = {split_pair(a, b), split_pair(c2, d2)};
-                            w[m] = f32x4{a, b, c2, d2};
-                            *reinterpret_cast<u32x2 *>(to + (i * 64 + l) * 8 + 4 * (wave & 1)) = bits;
-                        }
-                    }
-                }
-            }
-        }
-        if (k + 1 < n) prepare(chunk_of(k + 1), vecs[(k + 1) & 1]);
-        // the wave's columns of v: rows 32 b + 4 g + {0..3} and + 16
+        const bool more = k + 1 < n;  // (the last chunk is fetched again: a branch here would wait for the loads)
+        // the wave's columns of v: rows 32 b + 4 g + {0..3} and + 16; row of L 16 m + r
         In<T> fv[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
             fv[b] = tile_cols<T, kVCH>(tileV, 32 * b + 4 * g, 32 * b + 16 + 4 * g, [&](int q) { return 16 * wave + 4 * q; });
-        f32x4 x[4];
-        to_floats(fv[0], x[0], x[1]);
-        to_floats(fv[1], x[2], x[3]);
+        const float end = vec.end[0];
+
+        // S^T L (y[m]: row of L 16 m + r, columns 16 wave + 4 g + e), and W's column tile of
+        // this wave (w[m]: the same row, rows of R 16 wave + 4 g + e)
+        f32x4 y[4], w[4], x[4];
+        Sum<T, NX> fx[2];
+        auto enter = [&](int b) {  // the scaled rows 32 b .. of v
+            to_floats(fv[b], x[2 * b], x[2 * b + 1]);
+#pragma unroll
+            for (int m = 2 * b; m < 2 * b + 2; ++m) {
+                const f32x4 scale = *reinterpret_cast<const f32x4 *>(vec.in + 16 * m + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[m][e] *= scale[e];
+            }
+            fx[b] = to_sum<T, NX>(x[2 * b], x[2 * b + 1]);
+            pin(fx[b]);
+        };
         if constexpr (kOut) {
-            // e^G S^T L + D v, then W v
+            In<T> fl[2][4], fr[2];
+            Sum<T, NR> fs[2];
+            auto read = [&](int b) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) fl[b & 1][m] = tile_row<T, NCH>(tileL, 16 * m + r, 4 * b + g);
+                fr[b & 1] = tile_row<T, NCH>(tileR, 16 * wave + r, 4 * b + g);
+            };
+#pragma unroll
+            for (int m = 0; m < 4; ++m) y[m] = w[m] = f32x4{0, 0, 0, 0};
+            read(0);
+            fs[0] = to_sum<T, NR>(S[0], S[1]);
+            fence();
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                if (b + 1 < KB) {
+                    read(b + 1);
+                    fs[(b + 1) & 1] = to_sum<T, NR>(S[2 * b + 2], S[2 * b + 3]);
+                }
+                mma_right<4>(w, fr[b & 1], fl[b & 1]);
+                mma_right<4>(y, fs[b & 1], fl[b & 1]);
+                // the last two have the time to form the operands of the next phase
+                if (b >= KB - 2) enter(b - (KB - 2));
+                interleave<sizeof(T) == 2 ? 5 : 10, sizeof(T) == 2 ? 4 + 4 * NR : 64, sizeof(T) == 2 ? 5 : 0>();
+                fence();
+            }
+        } else {
+            enter(0);
+            enter(1);
+        }
+        // The next chunk's rows on their way, ahead of the stores: what waits for them does
+        // not wait for those.
+        pL += more ? dL : 0;
+        pR += more ? dR : 0;
+        pV += more ? dV : 0;
+        fetch(pL, pR, pV, rows_of(more ? k + 1 : k));
+        if constexpr (kKeep) {
+            keep_state(pK);
+            pK += dK;
+        }
+        // S = e^{Gc} S + R^T (scaled v);  beside it W's decays
+        In<T> fc[2][2];  // [parity of the time block][tile of the pair]
+        auto read_cols_of = [&](int b, int t) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+                fc[t][o] = tile_cols<T, NCH>(tileR, 32 * t + 4 * g, 32 * t + 16 + 4 * g,
+                                             [&](int q) { return 32 * b + 8 * q + 4 * o; });
+        };
+        auto decay = [&](int b) {
+#pragma unroll
+            for (int m = 2 * b; m < 2 * b + 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][e] *= end;
+        };
+        // W's tile m, in the wave that is the W-th.  Off the diagonal a decay is a product over
+        // the step between the tiles: one exponential a row and one a column.
+        f32x4 far;
+        auto weigh = [&](auto is, int m) {
+            constexpr int W = decltype(is)::value;
+            // the step between a tile on the diagonal and those beside it: the last of the
+            // earlier one
+            constexpr int ref = kRev ? (W ? 16 * W - 1 : 0) : 16 * W + 15;
+            const int i = 16 * m + r;
+            const float ihi = vec.hi[i], ilo = vec.lo[i], rhi = vec.hi[ref], rlo = vec.lo[ref];
+            if (m == W) {
+                const f32x4 hi = *reinterpret_cast<const f32x4 *>(vec.hi + 16 * W + 4 * g);
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(vec.lo + 16 * W + 4 * g);
+                const f32x4 dts = *reinterpret_cast<const f32x4 *>(vec.dt + 16 * W + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float q = (rhi - hi[e]) + (rlo - lo[e]);
+                    far[e] = kRev ? exp2_hw(-q) : exp2_hw(q) * dts[e];
+                    const int j = 16 * W + 4 * g + e;
+                    float d = (ihi - hi[e]) + (ilo - lo[e]);
+                    if (kRev) d = -d;
+                    d = (kRev ? j >= i : j <= i) ? d : -__builtin_inff();  // (no branch around the exponential)
+                    // the skip is the diagonal's
+                    w[m][e] = __builtin_fmaf(w[m][e], exp2_hw(d) * (kRev ? vec.dt[i] : dts[e]), i == j ? D : 0.0f);
+                }
+            } else {
+                const float d = (ihi - rhi) + (ilo - rlo);
+                const float f = kRev ? exp2_hw(-d) * vec.dt[i] : exp2_hw(d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[m][e] *= f * far[e];
+            }
+            // the half of a fragment that these four are
+            E<T> *to = tri + (kRev ? tri_upper(m, W / 2) : tri_lower(m, W / 2)) * kFrag + l * 8 + 4 * (W & 1);
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<f32x4 *>(to) = w[m];
+            } else {
+                float a = w[m][0], b = w[m][1], c = w[m][2], d = w[m][3];
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+                    const uint32_t ab = split_pair(a, b), cd = split_pair(c, d);
+                    *reinterpret_cast<u32x2 *>(to + i * 512) = u32x2{ab, cd};
+                }
+            }
+        };
+        auto update = [&](auto is) {
+            constexpr int W = decltype(is)::value;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                read_cols_of(b, 1);
+                if (b + 1 < KB) decay(b + 1);
+                mma_left<2>(S + 2 * b, fc[0], fx[0]);
+                if (b + 1 < KB) read_cols_of(b + 1, 0);
+                mma_left<2>(S + 2 * b, fc[1], fx[1]);
+                if constexpr (kOut) {
+                    // from the diagonal's tile on to the corner of the triangle
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i * KB / 4 == b && (kRev ? W - i >= 0 : W + i < 4)) weigh(is, kRev ? W - i : W + i);
+                }
+                interleave<sizeof(T) == 2 ? 4 : 0, sizeof(T) == 2 ? 4 * NX : 32, sizeof(T) == 2 ? 4 : 0>();
+                fence();
+            }
+        };
+        read_cols_of(0, 0);
+        decay(0);
+        fence();
+        if constexpr (kOut) {
+            if (wave == 0) update(std::integral_constant<int, 0>{});
+            else if (wave == 1) update(std::integral_constant<int, 1>{});
+            else if (wave == 2) update(std::integral_constant<int, 2>{});
+            else update(std::integral_constant<int, 3>{});
+            settle();
+        } else {
+            update(std::integral_constant<int, 0>{});
+        }
+        if constexpr (kOut) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const f32x4 scale = *reinterpret_cast<const f32x4 *>(vec.out + 16 * m + 4 * g);
+                const float scale = vec.out[16 * m + r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[m][e] = __builtin_fmaf(D, x[m][e], scale[e] * y[m][e]);
+                for (int e = 0; e < 4; ++e) y[m][e] *= scale;
             }
-            __syncthreads();
+        }
+        __syncthreads();
+        store(more ? k + 1 : k);
+        if constexpr (kOut) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 // row tiles with a fragment in block b: all four, but two in one of the blocks
                 constexpr int kAll = kRev ? 1 : 0;
                 auto frag = [&](int m) {
-                    const E<T> *at = tri + (kRev ? tri_upper(m, b) : tri_lower(m, b)) * (kTri / kTriFrags);
+                    const E<T> *at = tri + (kRev ? tri_upper(m, b) : tri_lower(m, b)) * kFrag;
                     if constexpr (sizeof(T) == 4) {
                         const f32x4 *q = reinterpret_cast<const f32x4 *>(at + l * 8);
                         return F32x8{q[0], q[1]};
@@ -249,59 +394,33 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
                 };
                 if (b == kAll) {
                     const Sum<T, NW> a[4] = {frag(0), frag(1), frag(2), frag(3)};
-                    mma_left<4>(y, a, fv[b]);
+                    mma_right<4>(y, fv[b], a);
                 } else {
                     constexpr int m0 = kRev ? 0 : 2;
                     const Sum<T, NW> a[2] = {frag(m0), frag(m0 + 1)};
-                    mma_left<2>(y + m0, a, fv[b]);
+                    mma_right<2>(y + m0, fv[b], a);
                 }
             }
+            store_out<kFast>(pO, p.sout.t, p.out_bf16, rows_of(k), 16 * wave + 4 * g, p.P - col0, r, y);
+            pO += dO;
         }
-        // S = e^{Gc} S + R^T (scaled v)
-        const float end = vec.end[0];
-        Sum<T, NX> fx[2];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4 scale = *reinterpret_cast<const f32x4 *>(vec.in + 16 * m + 4 * g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[m][e] *= scale[e];
-        }
-        fx[0] = to_sum<T, NX>(x[0], x[1]);
-        fx[1] = to_sum<T, NX>(x[2], x[3]);
-#pragma unroll
-        for (int m = 0; m < ND / 16; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[m][e] *= end;
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2) {
-                In<T> fr[2];
-#pragma unroll
-                for (int o = 0; o < 2; ++o)
-                    fr[o] = tile_cols<T, NCH>(tileR, 32 * t2 + 4 * g, 32 * t2 + 16 + 4 * g,
-                                              [&](int q) { return 32 * b + 8 * q + 4 * o; });
-                mma_left<2>(S + 2 * b, fr, fx[t2]);
-            }
-        if constexpr (kOut) {
-            const long long at = out_at + t * p.sout.t;
-            if (p.out_bf16)
-                store_column<bf16_t, false>(static_cast<bf16_t *>(p.out) + at, p.sout.t, rows, g, col, mine, y);
-            else
-                store_column<float, false>(static_cast<float *>(p.out) + at, p.sout.t, rows, g, col, mine, y);
-        }
+        __syncthreads();
     }
     if constexpr (kEnd) {
         keep_state(end_to);
-        if (blockIdx.z == 0 && wave == kWaves - 1 && l == 0) p.ws.decay[slot] = exp2_of(passed);
+        if (blockIdx.z == 0) {
+            double *part = reinterpret_cast<double *>(vecs);
+            __syncthreads();
+            if (l == 0) part[wave] = passed;
+            __syncthreads();
+            if (threadIdx.x == 0) p.ws.decay[slot] = exp2_of((part[0] + part[1]) + (part[2] + part[3]));
+        }
     } else if (p.sL && mine && last) {
 #pragma unroll
         for (int m = 0; m < ND / 16; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 32 * (m / 2) + 8 * g + 4 * (m % 2) + e;
-                if (row < p.N) p.sL[state_at + (long long)row * p.P] = S[m][e];
-            }
+            for (int e = 0; e < 4; ++e)
+                if (row_of(m, e) < p.N) p.sL[state_at + (long long)row_of(m, e) * p.P] = S[m][e];
     }
 }
 
@@ -376,7 +495,8 @@ hipError_t launch_heads_scan(const HeadsArgs &a, const HeadsScan &p, bool revers
     const bool bf16 = p.in_bf16 && p.v_bf16, same = p.in_bf16 == p.v_bf16;
     const int es = p.in_bf16 ? 2 : 4;
     const bool fast = same && heads_fast(p.L, p.sL_, a.N, es, a, a.groups) && heads_fast(p.R, p.sR, a.N, es, a, a.groups) &&
-                      heads_fast(p.v, p.sv, a.P, es, a, a.h);
+                      heads_fast(p.v, p.sv, a.P, es, a, a.h) &&
+                      (!p.out || heads_fast(p.out, p.sout, a.P, p.out_bf16 ? 2 : 4, a, a.h));
     return bf16 ? scan_typed<bf16_t>(a, p, reverse, fast, stream) : scan_typed<float>(a, p, reverse, fast, stream);
 }
 
