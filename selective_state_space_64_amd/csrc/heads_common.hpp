@@ -275,10 +275,26 @@ struct Vec {
     float hi[64], lo[64], dt[64], out[64], in[64], end[4];
 };
 
-// Element loads of a [steps] column of either type.
+// An element of a [steps] column of either type, as it was loaded: what would convert
+// it here would wait for it here, and so would the end of a branch by type.
+struct RawStep {
+    uint16_t lo, hi;
+    __device__ inline void load(const void *p, long long at, int bf16)
+    {
+        const char *const q = static_cast<const char *>(p) + at * (bf16 ? 2 : 4);
+        lo = *reinterpret_cast<const uint16_t *>(q);
+        hi = *reinterpret_cast<const uint16_t *>(q + (bf16 ? 0 : 2));
+    }
+    __device__ inline float value(int bf16) const
+    {
+        return __uint_as_float(bf16 ? uint32_t(lo) << 16 : uint32_t(hi) << 16 | lo);
+    }
+};
 __device__ inline float load_step(const void *p, long long at, int bf16)
 {
-    return bf16 ? io<bf16_t>::load1(static_cast<const bf16_t *>(p) + at) : static_cast<const float *>(p)[at];
+    RawStep raw;
+    raw.load(p, at, bf16);
+    return raw.value(bf16);
 }
 
 // ---------------------------------------------------------------- workspace

@@ -91,13 +91,12 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     if (kEnd && last) return;  // nothing follows
     const DeltaSeq &seq = seg.s;
     const int c0 = seg.c0, n = seg.c1 - seg.c0;
-    const int col0 = int(blockIdx.z) * kCols, col = col0 + 16 * wave + r;
-    const bool mine = col < p.P, kept = col0 + 16 * wave < p.ws.Pp;  // (of whole tiles)
+    const int col0 = int(blockIdx.z) * kCols, wcol = 16 * wave, col = col0 + wcol + r;  // wcol: the wave's first of them
     const long long state_at = ((long long)seg.seq * p.h + head) * p.N * (long long)p.P + col;
     const long long slot = (long long)blockIdx.x * p.h + head;
     // this segment's place in ends, the one before it in the run's order, and the last one's
     float *const end_to = p.ws.ends + slot * p.ws.state;
-    const float *const entry = p.ws.ends + (slot + (kRev ? p.h : -p.h)) * p.ws.state + col;
+    const float *const entry = p.ws.ends + (slot + (kRev ? p.h : -p.h)) * p.ws.state;
     float *const initial = p.ws.ends + (slot + (long long)p.h * (kRev ? -seg.index : seg.behind)) * p.ws.state;
     const bool split = p.ws.seg_chunks > 0 && !(first && last);
     const float A = p.A[head], bias = p.bias ? p.bias[head] : 0.0f, D = p.D ? p.D[head] : 0.0f;
@@ -105,39 +104,47 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     // S: tiles 2 b and 2 b + 1 hold the rows 32 b + 8 g + {0..3} and + {4..7}
     f32x4 S[ND / 16];
     auto row_of = [&](int m, int e) { return 32 * (m / 2) + 8 * g + 4 * (m % 2) + e; };
-#pragma unroll
-    for (int m = 0; m < ND / 16; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = row_of(m, e);
-            float s = 0.0f;
-            if (!first) {
-                if (!kEnd && kept && row < p.ws.Nr) s = entry[(long long)row * p.ws.Pp];
-            } else if (p.s0) {
-                // a split sequence's initial state: kept by the ends' run, because sL may
-                // be the same memory and the last segment may end before the first begins
-                if (split && !kEnd) {
-                    if (kept && row < p.ws.Nr) s = initial[(long long)row * p.ws.Pp + col];
-                } else if (mine && row < p.N) {
-                    s = p.s0[state_at + (long long)row * p.P];
-                }
-            }
-            S[m][e] = s;
-        }
-    // rows behind Nr lie behind the record's end and are not stored
-    const uint32_t keep_off = kept ? uint32_t(8 * g * p.ws.Pp + col) * 4u : kOutside;
+    // a record's rows behind Nr lie behind its end: they read as 0 and are not stored
+    auto record_off = [&]() {
+        uint32_t off = col0 + wcol < p.ws.Pp ? uint32_t(8 * g * p.ws.Pp + col) * 4u : kOutside;
+        opaque(off);
+        return off;
+    };
+    auto record_row = [&](int m, int e) { return uint32_t((32 * (m / 2) + 4 * (m % 2) + e) * p.ws.Pp) * 4u; };
     auto keep_state = [&](float *to) {
         const auto buf = buffer_of(to, p.ws.state * 4);
-        uint32_t off = keep_off;
-        opaque(off);
+        const uint32_t off = record_off();
 #pragma unroll
         for (int m = 0; m < ND / 16; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][e]), buf,
-                                                      off + uint32_t((32 * (m / 2) + 4 * (m % 2) + e) * p.ws.Pp) * 4u, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][e]), buf, off + record_row(m, e), 0, 0);
     };
-    if (kEnd && first && p.s0) keep_state(initial);
+    auto load_state = [&](const float *from) {
+        const auto buf = buffer_of(from, p.ws.state * 4);
+        const uint32_t off = record_off();
+#pragma unroll
+        for (int m = 0; m < ND / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[m][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, off + record_row(m, e), 0, 0));
+    };
+#pragma unroll
+    for (int m = 0; m < ND / 16; ++m) S[m] = f32x4{0, 0, 0, 0};
+    if (!first) {
+        if (!kEnd) load_state(entry);
+    } else if (p.s0 && split && !kEnd) {
+        // a split sequence's initial state, kept by the ends' run: sL may be the same
+        // memory, and the last segment may end before the first begins
+        load_state(initial);
+    } else if (p.s0) {
+#pragma unroll
+        for (int m = 0; m < ND / 16; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col < p.P && row_of(m, e) < p.N) S[m][e] = p.s0[state_at + (long long)row_of(m, e) * p.P];
+        if (kEnd) keep_state(initial);
+    }
 
     // the chunks in the order of the run, and where each one's rows begin
     const int ein = p.in_bf16 ? 2 : 4, ev = p.v_bf16 ? 2 : 4, eo = p.out_bf16 ? 2 : 4;
@@ -152,35 +159,35 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
     float *pK = p.keep + (((long long)seq.chunk0 + chunk_of(0)) * p.h + head) * p.ws.state;
     const long long dK = (kRev ? -p.h : p.h) * p.ws.state;
     const long long dt_at = seq.batch * p.sdt.b + seq.first * p.sdt.t + head * p.sdt.h;
+    auto rows_of = [&](int k) { return min(seq.len - chunk_of(k) * kDeltaChunk, kDeltaChunk); };
 
     TileIn<T, NCH, kFast> inL, inR;
     TileIn<T, kVCH, kFast> inV;
     inL.init(p.sL_.t, p.N);
     inR.init(p.sR.t, p.N);
     inV.init(p.sv.t, p.P - col0);
-    auto rows_of = [&](int k) { return min(seq.len - chunk_of(k) * kDeltaChunk, kDeltaChunk); };
-    auto fetch = [&](const char *l_at, const char *r_at, const char *v_at, int rows) {
-        if constexpr (kOut) inL.fetch(l_at, p.sL_.t, rows);
-        inR.fetch(r_at, p.sR.t, rows);
-        inV.fetch(v_at, p.sv.t, rows);
+    // the chunk's rows on their way, and from there to the tiles
+    auto fetch = [&](int rows) {
+        if constexpr (kOut) inL.fetch(pL, p.sL_.t, rows);
+        inR.fetch(pR, p.sR.t, rows);
+        inV.fetch(pV, p.sv.t, rows);
     };
-    auto store = [&](int k) {
-        const int rows = rows_of(k);
+    auto store = [&](int rows) {
         if constexpr (kOut) inL.store(tileL, pL, p.sL_.t, rows, p.N, p.in_bf16);
         inR.store(tileR, pR, p.sR.t, rows, p.N, p.in_bf16);
         inV.store(tileV, pV, p.sv.t, rows, p.P - col0, p.v_bf16);
     };
-    // the wave's chunk of those from `base` on
-    float raw = 0.0f;
+    // the raw steps of the wave's chunk of those from `base` on (or of the last one: a load
+    // in a branch would be waited for where the branch ends)
+    RawStep raw{};
     auto load_raw = [&](int base) {
-        if (wave < kAhead && base + wave < n)
-            raw = load_step(p.dt, dt_at + ((long long)chunk_of(base + wave) * kDeltaChunk + min(l, rows_of(base + wave) - 1)) * p.sdt.t,
-                            p.in_bf16);
+        const int k = min(base + wave, n - 1);
+        raw.load(p.dt, dt_at + ((long long)chunk_of(k) * kDeltaChunk + min(l, rows_of(k) - 1)) * p.sdt.t, p.in_bf16);
     };
     double passed = 0.0;  // the wave's part of the segment's decay
     auto prepare = [&](int base) {
         if (wave >= kAhead || base + wave >= n) return;
-        const Decays d = decays(raw, bias, A, rows_of(base + wave));
+        const Decays d = decays(raw.value(p.in_bf16), bias, A, rows_of(base + wave));
         Vec &v = vecs[(base + wave) & (2 * kAhead - 1)];
         v.hi[l] = float(d.G);
         v.lo[l] = float(d.G - double(float(d.G)));
@@ -194,148 +201,155 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
 
     if (n > 0) {
         load_raw(0);
-        fetch(pL, pR, pV, rows_of(0));
+        fetch(rows_of(0));
         if constexpr (kOut)  // the halves of fragments on the far side of the diagonal stay 0
             for (int i = int(threadIdx.x); i < kTriFrags * kFrag; i += kThreads) tri[i] = E<T>(0);
         prepare(0);
         load_raw(kAhead);
-        store(0);
+        store(rows_of(0));
         __syncthreads();
     }
-    // Two barriers a chunk: all that reads the tiles stands before the first, where W is
-    // complete too; the next chunk's tiles are stored behind it, beside W v.  Between them
-    // each phase's fragments are read while the phase before it computes, and the vector
-    // work (terms, decays) takes turns with matrix instructions that do not wait for it.
-    for (int k = 0; k < n; ++k) {
-        const Vec &vec = vecs[k & (2 * kAhead - 1)];
-        if ((k & (kAhead - 1)) == 0) {
-            prepare(k + kAhead);
-            load_raw(k + 2 * kAhead);
-        }
-        const bool more = k + 1 < n;  // (the last chunk is fetched again: a branch here would wait for the loads)
-        // the wave's columns of v: rows 32 b + 4 g + {0..3} and + 16; row of L 16 m + r
-        In<T> fv[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-            fv[b] = tile_cols<T, kVCH>(tileV, 32 * b + 4 * g, 32 * b + 16 + 4 * g, [&](int q) { return 16 * wave + 4 * q; });
-        const float end = vec.end[0];
 
-        // S^T L (y[m]: row of L 16 m + r, columns 16 wave + 4 g + e), and W's column tile of
-        // this wave (w[m]: the same row, rows of R 16 wave + 4 g + e)
-        f32x4 y[4], w[4], x[4];
-        Sum<T, NX> fx[2];
-        auto enter = [&](int b) {  // the scaled rows 32 b .. of v
-            to_floats(fv[b], x[2 * b], x[2 * b + 1]);
+    // All chunks, as the wave that is the W-th.  Each phase's fragments are read while the
+    // phase before it computes, and the vector work (terms, decays) takes turns with matrix
+    // instructions that do not wait for it.
+    auto run = [&](auto is) {
+        constexpr int W = decltype(is)::value;
+        for (int k = 0; k < n; ++k) {
+            const Vec &vec = vecs[k & (2 * kAhead - 1)];
+            if ((k & (kAhead - 1)) == 0) prepare(k + kAhead);
+            load_raw(k + 1 + kAhead);  // for the next chunk's prepare()
+            const bool more = k + 1 < n;  // (the last chunk is fetched again: a branch here would wait for the loads)
+            const int next_rows = rows_of(more ? k + 1 : k);
+            pL += more ? dL : 0;
+            pR += more ? dR : 0;
+            pV += more ? dV : 0;
+            // the wave's columns of v: rows 32 b + 4 g + {0..3} and + 16
+            In<T> fv[2];
 #pragma unroll
-            for (int m = 2 * b; m < 2 * b + 2; ++m) {
-                const f32x4 scale = *reinterpret_cast<const f32x4 *>(vec.in + 16 * m + 4 * g);
+            for (int b = 0; b < 2; ++b)
+                fv[b] = tile_cols<T, kVCH>(tileV, 32 * b + 4 * g, 32 * b + 16 + 4 * g, [&](int q) { return wcol + 4 * q; });
+            const float end = vec.end[0];
+
+            // S^T L (y[m]: row of L 16 m + r, columns 4 g + e of the tile), and W's column tile of
+            // this wave (w[m]: the same row, rows of R 16 W + 4 g + e)
+            f32x4 y[4], w[4];
+            Sum<T, NX> fx[2];
+            auto enter = [&](int b) {  // the scaled rows 32 b .. of v
+                f32x4 x[2];
+                to_floats(fv[b], x[0], x[1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[m][e] *= scale[e];
-            }
-            fx[b] = to_sum<T, NX>(x[2 * b], x[2 * b + 1]);
-            pin(fx[b]);
-        };
-        if constexpr (kOut) {
-            In<T> fl[2][4], fr[2];
-            Sum<T, NR> fs[2];
-            auto read = [&](int b) {
+                for (int m = 0; m < 2; ++m) {
+                    const f32x4 scale = *reinterpret_cast<const f32x4 *>(vec.in + 32 * b + 16 * m + 4 * g);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) fl[b & 1][m] = tile_row<T, NCH>(tileL, 16 * m + r, 4 * b + g);
-                fr[b & 1] = tile_row<T, NCH>(tileR, 16 * wave + r, 4 * b + g);
+                    for (int e = 0; e < 4; ++e) x[m][e] *= scale[e];
+                }
+                fx[b] = to_sum<T, NX>(x[0], x[1]);
+                pin(fx[b]);
             };
+            if constexpr (kOut) {
+                In<T> fl[2][4], fr[2];
+                Sum<T, NR> fs[2];
+                auto read = [&](int b) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) y[m] = w[m] = f32x4{0, 0, 0, 0};
-            read(0);
-            fs[0] = to_sum<T, NR>(S[0], S[1]);
-            fence();
+                    for (int m = 0; m < 4; ++m) fl[b & 1][m] = tile_row<T, NCH>(tileL, 16 * m + r, 4 * b + g);
+                    fr[b & 1] = tile_row<T, NCH>(tileR, 16 * W + r, 4 * b + g);
+                };
+                auto form = [&](int b) {
+                    fs[b & 1] = to_sum<T, NR>(S[2 * b], S[2 * b + 1]);
+                    pin(fs[b & 1]);
+                };
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                if (b + 1 < KB) {
-                    read(b + 1);
-                    fs[(b + 1) & 1] = to_sum<T, NR>(S[2 * b + 2], S[2 * b + 3]);
-                }
-                mma_right<4>(w, fr[b & 1], fl[b & 1]);
-                mma_right<4>(y, fs[b & 1], fl[b & 1]);
-                // the last two have the time to form the operands of the next phase
-                if (b >= KB - 2) enter(b - (KB - 2));
-                interleave<sizeof(T) == 2 ? 5 : 10, sizeof(T) == 2 ? 4 + 4 * NR : 64, sizeof(T) == 2 ? 5 : 0>();
+                for (int m = 0; m < 4; ++m) y[m] = w[m] = f32x4{0, 0, 0, 0};
+                read(0);
+                form(0);
                 fence();
-            }
-        } else {
-            enter(0);
-            enter(1);
-        }
-        // The next chunk's rows on their way, ahead of the stores: what waits for them does
-        // not wait for those.
-        pL += more ? dL : 0;
-        pR += more ? dR : 0;
-        pV += more ? dV : 0;
-        fetch(pL, pR, pV, rows_of(more ? k + 1 : k));
-        if constexpr (kKeep) {
-            keep_state(pK);
-            pK += dK;
-        }
-        // S = e^{Gc} S + R^T (scaled v);  beside it W's decays
-        In<T> fc[2][2];  // [parity of the time block][tile of the pair]
-        auto read_cols_of = [&](int b, int t) {
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
-                fc[t][o] = tile_cols<T, NCH>(tileR, 32 * t + 4 * g, 32 * t + 16 + 4 * g,
-                                             [&](int q) { return 32 * b + 8 * q + 4 * o; });
-        };
-        auto decay = [&](int b) {
-#pragma unroll
-            for (int m = 2 * b; m < 2 * b + 2; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[m][e] *= end;
-        };
-        // W's tile m, in the wave that is the W-th.  Off the diagonal a decay is a product over
-        // the step between the tiles: one exponential a row and one a column.
-        f32x4 far;
-        auto weigh = [&](auto is, int m) {
-            constexpr int W = decltype(is)::value;
-            // the step between a tile on the diagonal and those beside it: the last of the
-            // earlier one
-            constexpr int ref = kRev ? (W ? 16 * W - 1 : 0) : 16 * W + 15;
-            const int i = 16 * m + r;
-            const float ihi = vec.hi[i], ilo = vec.lo[i], rhi = vec.hi[ref], rlo = vec.lo[ref];
-            if (m == W) {
-                const f32x4 hi = *reinterpret_cast<const f32x4 *>(vec.hi + 16 * W + 4 * g);
-                const f32x4 lo = *reinterpret_cast<const f32x4 *>(vec.lo + 16 * W + 4 * g);
-                const f32x4 dts = *reinterpret_cast<const f32x4 *>(vec.dt + 16 * W + 4 * g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float q = (rhi - hi[e]) + (rlo - lo[e]);
-                    far[e] = kRev ? exp2_hw(-q) : exp2_hw(q) * dts[e];
-                    const int j = 16 * W + 4 * g + e;
-                    float d = (ihi - hi[e]) + (ilo - lo[e]);
-                    if (kRev) d = -d;
-                    d = (kRev ? j >= i : j <= i) ? d : -__builtin_inff();  // (no branch around the exponential)
-                    // the skip is the diagonal's
-                    w[m][e] = __builtin_fmaf(w[m][e], exp2_hw(d) * (kRev ? vec.dt[i] : dts[e]), i == j ? D : 0.0f);
+                for (int b = 0; b < KB; ++b) {
+                    if (b + 1 < KB) {
+                        read(b + 1);
+                        form(b + 1);
+                    }
+                    // (the tiles of the triangle: from the diagonal's on, or up to it)
+                    constexpr int m0 = kRev ? 0 : W, kTiles = kRev ? W + 1 : 4 - W;
+                    mma_right<kTiles>(w + m0, fr[b & 1], fl[b & 1] + m0);
+                    mma_right<4>(y, fs[b & 1], fl[b & 1]);
+                    // the last two have the time to form the operands of the next phase
+                    if (b >= KB - 2) enter(b - (KB - 2));
+                    interleave<sizeof(T) == 2 ? 5 : 10, sizeof(T) == 2 ? kTiles + 4 * NR : 64, sizeof(T) == 2 ? 5 : 0>();
+                    fence();
                 }
             } else {
-                const float d = (ihi - rhi) + (ilo - rlo);
-                const float f = kRev ? exp2_hw(-d) * vec.dt[i] : exp2_hw(d);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[m][e] *= f * far[e];
+                enter(0);
+                enter(1);
             }
-            // the half of a fragment that these four are
-            E<T> *to = tri + (kRev ? tri_upper(m, W / 2) : tri_lower(m, W / 2)) * kFrag + l * 8 + 4 * (W & 1);
-            if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<f32x4 *>(to) = w[m];
-            } else {
-                float a = w[m][0], b = w[m][1], c = w[m][2], d = w[m][3];
+            // The next chunk's rows on their way, ahead of the stores: what waits for them does
+            // not wait for those.
+            fetch(next_rows);
+            if constexpr (kKeep) {
+                keep_state(pK);
+                pK += dK;
+            }
+            // S = e^{Gc} S + R^T (scaled v);  beside it W's decays
+            In<T> fc[2][2];  // [parity of the time block][tile of the pair]
+            auto read_cols_of = [&](int b, int t) {
 #pragma unroll
-                for (int i = 0; i < NW; ++i) {
-                    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-                    const uint32_t ab = split_pair(a, b), cd = split_pair(c, d);
-                    *reinterpret_cast<u32x2 *>(to + i * 512) = u32x2{ab, cd};
+                for (int o = 0; o < 2; ++o)
+                    fc[t][o] = tile_cols<T, NCH>(tileR, 32 * t + 4 * g, 32 * t + 16 + 4 * g,
+                                                 [&](int q) { return 32 * b + 8 * q + 4 * o; });
+            };
+            auto decay = [&](int b) {
+#pragma unroll
+                for (int m = 2 * b; m < 2 * b + 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[m][e] *= end;
+            };
+            // W's row tile m.  Off the diagonal a decay is a product
+            // over the step between the tiles: one exponential a row and one a column.
+            f32x4 far;
+            auto weigh = [&](int m) {
+                // the last step of the earlier tile
+                const int ref = kRev ? (W ? 16 * W - 1 : 0) : 16 * W + 15;
+                const int at = 16 * m + r;
+                const float ihi = vec.hi[at], ilo = vec.lo[at], rhi = vec.hi[ref], rlo = vec.lo[ref];
+                if (m == W) {
+                    const f32x4 hi = *reinterpret_cast<const f32x4 *>(vec.hi + 16 * W + 4 * g);
+                    const f32x4 lo = *reinterpret_cast<const f32x4 *>(vec.lo + 16 * W + 4 * g);
+                    const f32x4 dts = *reinterpret_cast<const f32x4 *>(vec.dt + 16 * W + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float q = (rhi - hi[e]) + (rlo - lo[e]);
+                        far[e] = kRev ? exp2_hw(-q) : exp2_hw(q) * dts[e];
+                        const int j = 16 * W + 4 * g + e;
+                        float d = (ihi - hi[e]) + (ilo - lo[e]);
+                        if (kRev) d = -d;
+                        d = (kRev ? j >= at : j <= at) ? d : -__builtin_inff();  // (no branch around the exponential)
+                        // the skip is the diagonal's
+                        w[m][e] = __builtin_fmaf(w[m][e], exp2_hw(d) * (kRev ? vec.dt[at] : dts[e]), at == j ? D : 0.0f);
+                    }
+                } else {
+                    const float d = (ihi - rhi) + (ilo - rlo);
+                    const float f = kRev ? exp2_hw(-d) * vec.dt[at] : exp2_hw(d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[m][e] *= f * far[e];
                 }
-            }
-        };
-        auto update = [&](auto is) {
-            constexpr int W = decltype(is)::value;
+                // the half of a fragment that these four are
+                E<T> *to = tri + (kRev ? tri_upper(m, W / 2) : tri_lower(m, W / 2)) * kFrag + l * 8 + 4 * (W & 1);
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<f32x4 *>(to) = w[m];
+                } else {
+                    float v0 = w[m][0], v1 = w[m][1], v2 = w[m][2], v3 = w[m][3];
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) {
+                        typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+                        const uint32_t ab = split_pair(v0, v1), cd = split_pair(v2, v3);
+                        *reinterpret_cast<u32x2 *>(to + q * 512) = u32x2{ab, cd};
+                    }
+                }
+            };
+            read_cols_of(0, 0);
+            decay(0);
+            fence();
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 read_cols_of(b, 1);
@@ -346,66 +360,64 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
                 if constexpr (kOut) {
                     // from the diagonal's tile on to the corner of the triangle
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i * KB / 4 == b && (kRev ? W - i >= 0 : W + i < 4)) weigh(is, kRev ? W - i : W + i);
+                    for (int q = 0; q < 4; ++q)
+                        if (q * KB / 4 == b && (kRev ? W - q >= 0 : W + q < 4)) weigh(kRev ? W - q : W + q);
                 }
                 interleave<sizeof(T) == 2 ? 4 : 0, sizeof(T) == 2 ? 4 * NX : 32, sizeof(T) == 2 ? 4 : 0>();
                 fence();
             }
-        };
-        read_cols_of(0, 0);
-        decay(0);
-        fence();
-        if constexpr (kOut) {
-            if (wave == 0) update(std::integral_constant<int, 0>{});
-            else if (wave == 1) update(std::integral_constant<int, 1>{});
-            else if (wave == 2) update(std::integral_constant<int, 2>{});
-            else update(std::integral_constant<int, 3>{});
-            settle();
-        } else {
-            update(std::integral_constant<int, 0>{});
-        }
-        if constexpr (kOut) {
+            if constexpr (kOut) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float scale = vec.out[16 * m + r];
+                for (int m = 0; m < 4; ++m) {
+                    const float scale = vec.out[16 * m + r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[m][e] *= scale;
-            }
-        }
-        __syncthreads();
-        store(more ? k + 1 : k);
-        if constexpr (kOut) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                // row tiles with a fragment in block b: all four, but two in one of the blocks
-                constexpr int kAll = kRev ? 1 : 0;
-                auto frag = [&](int m) {
-                    const E<T> *at = tri + (kRev ? tri_upper(m, b) : tri_lower(m, b)) * kFrag;
-                    if constexpr (sizeof(T) == 4) {
-                        const f32x4 *q = reinterpret_cast<const f32x4 *>(at + l * 8);
-                        return F32x8{q[0], q[1]};
-                    } else {
-                        Frag<NW> f;
-#pragma unroll
-                        for (int i = 0; i < NW; ++i) f.t[i] = *reinterpret_cast<const bf16x8 *>(at + (i * 64 + l) * 8);
-                        return f;
-                    }
-                };
-                if (b == kAll) {
-                    const Sum<T, NW> a[4] = {frag(0), frag(1), frag(2), frag(3)};
-                    mma_right<4>(y, fv[b], a);
-                } else {
-                    constexpr int m0 = kRev ? 0 : 2;
-                    const Sum<T, NW> a[2] = {frag(m0), frag(m0 + 1)};
-                    mma_right<2>(y + m0, fv[b], a);
+                    for (int e = 0; e < 4; ++e) y[m][e] *= scale;
                 }
             }
-            store_out<kFast>(pO, p.sout.t, p.out_bf16, rows_of(k), 16 * wave + 4 * g, p.P - col0, r, y);
-            pO += dO;
+            __syncthreads();  // W is complete, the tiles have been read
+            store(next_rows);
+            if constexpr (kOut) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    // row tiles with a fragment in block b: all four, but two in one of the blocks
+                    constexpr int kAll = kRev ? 1 : 0;
+                    auto frag = [&](int m) {
+                        const E<T> *at = tri + (kRev ? tri_upper(m, b) : tri_lower(m, b)) * kFrag;
+                        if constexpr (sizeof(T) == 4) {
+                            const f32x4 *q = reinterpret_cast<const f32x4 *>(at + l * 8);
+                            return F32x8{q[0], q[1]};
+                        } else {
+                            Frag<NW> f;
+#pragma unroll
+                            for (int i = 0; i < NW; ++i) f.t[i] = *reinterpret_cast<const bf16x8 *>(at + (i * 64 + l) * 8);
+                            return f;
+                        }
+                    };
+                    if (b == kAll) {
+                        const Sum<T, NW> a[4] = {frag(0), frag(1), frag(2), frag(3)};
+                        mma_right<4>(y, fv[b], a);
+                    } else {
+                        constexpr int m0 = kRev ? 0 : 2;
+                        const Sum<T, NW> a[2] = {frag(m0), frag(m0 + 1)};
+                        mma_right<2>(y + m0, fv[b], a);
+                    }
+                }
+                store_out<kFast>(pO, p.sout.t, p.out_bf16, rows_of(k), wcol + 4 * g, p.P - col0, r, y);
+                pO += dO;
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        settle();
+    };
+    if constexpr (kOut) {
+        if (wave == 0) run(std::integral_constant<int, 0>{});
+        else if (wave == 1) run(std::integral_constant<int, 1>{});
+        else if (wave == 2) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, 3>{});
+    } else {
+        run(std::integral_constant<int, 0>{});
     }
+
     if constexpr (kEnd) {
         keep_state(end_to);
         if (blockIdx.z == 0) {
@@ -413,14 +425,18 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
             __syncthreads();
             if (l == 0) part[wave] = passed;
             __syncthreads();
-            if (threadIdx.x == 0) p.ws.decay[slot] = exp2_of((part[0] + part[1]) + (part[2] + part[3]));
+            if (threadIdx.x == 0) {
+                double sum = 0.0;
+                for (int i = 0; i < kWaves; ++i) sum += part[i];
+                p.ws.decay[slot] = exp2_of(sum);
+            }
         }
-    } else if (p.sL && mine && last) {
+    } else if (p.sL && last) {
 #pragma unroll
         for (int m = 0; m < ND / 16; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (row_of(m, e) < p.N) p.sL[state_at + (long long)row_of(m, e) * p.P] = S[m][e];
+                if (col < p.P && row_of(m, e) < p.N) p.sL[state_at + (long long)row_of(m, e) * p.P] = S[m][e];
     }
 }
 
@@ -472,20 +488,18 @@ hipError_t scan_run(const HeadsArgs &a, const HeadsScan &p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename T, int ND>
-hipError_t scan_sized(const HeadsArgs &a, const HeadsScan &p, bool reverse, bool fast, hipStream_t stream)
-{
-    if (reverse) return fast ? scan_run<T, ND, true, true>(a, p, stream) : scan_run<T, ND, true, false>(a, p, stream);
-    return fast ? scan_run<T, ND, false, true>(a, p, stream) : scan_run<T, ND, false, false>(a, p, stream);
-}
-
 template <typename T>
 hipError_t scan_typed(const HeadsArgs &a, const HeadsScan &p, bool reverse, bool fast, hipStream_t stream)
 {
     const int nd = heads_nd(a.N);
-    return nd == 64 ? scan_sized<T, 64>(a, p, reverse, fast, stream)
-         : nd == 128 ? scan_sized<T, 128>(a, p, reverse, fast, stream)
-                     : scan_sized<T, 256>(a, p, reverse, fast, stream);
+    auto sized = [&](auto n) {
+        constexpr int ND = decltype(n)::value;
+        if (reverse) return fast ? scan_run<T, ND, true, true>(a, p, stream) : scan_run<T, ND, true, false>(a, p, stream);
+        return fast ? scan_run<T, ND, false, true>(a, p, stream) : scan_run<T, ND, false, false>(a, p, stream);
+    };
+    return nd == 64 ? sized(std::integral_constant<int, 64>{})
+         : nd == 128 ? sized(std::integral_constant<int, 128>{})
+                     : sized(std::integral_constant<int, 256>{});
 }
 
 }  // namespace
