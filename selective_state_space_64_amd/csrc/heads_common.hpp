@@ -156,8 +156,9 @@ __device__ inline void pin(F32x8 &) {}
 // fetch() to store(), 16-byte loads from one buffer whose end stands for the
 // masks of rows; otherwise store() loads them element by element, of the type
 // that `bf16` says (fp32 compute takes either).
-template <typename T, int NCH, bool kFast> struct TileIn {
-    static constexpr int kPer = 64 * NCH / kThreads, kWords = int(sizeof(T) / 2);
+template <typename T, int NCH, bool kFast, int kThreads = 256> struct TileIn {
+    static constexpr int kPer = (64 * NCH + kThreads - 1) / kThreads, kWords = int(sizeof(T) / 2);
+    static constexpr bool kSpare = 64 * NCH < kThreads;  // threads without a chunk
     u32x4 raw[kFast ? kPer : 1][kWords];
     uint32_t off, run;  // of the thread's first chunk; from one of its rows to the next
     // rows `step` elements apart, columns [0, n) exist
@@ -191,6 +192,7 @@ template <typename T, int NCH, bool kFast> struct TileIn {
         } else {
             for (int i = 0; i < kPer; ++i) {
                 const int at = int(threadIdx.x) + i * kThreads, t = at / NCH, c = at % NCH;
+                if (kSpare && t >= 64) return;
                 const long long row = (long long)min(t, rows - 1) * step;
                 const int count = t < rows ? n - c * 8 : 0;
                 if (sizeof(T) == 2 || !bf16) {
@@ -209,6 +211,7 @@ template <typename T, int NCH, bool kFast> struct TileIn {
     __device__ static inline void put(E<T> *tile, int i, const u32x4 *w)
     {
         const int at = int(threadIdx.x) + i * kThreads;
+        if (kSpare && at >= 64 * NCH) return;
         u32x4 *to = reinterpret_cast<u32x4 *>(tile + chunk_at<NCH>(at / NCH, at % NCH));
 #pragma unroll
         for (int k = 0; k < kWords; ++k) to[k] = w[k];
@@ -345,7 +348,7 @@ struct HeadsWs {
 inline int heads_parts(int batch, int seqlen, int groups, int h, int num_seqs)
 {
     const long long wgs = delta_chunks(batch, seqlen, num_seqs) * groups, rep = h / groups;
-    long long parts = (512 + wgs - 1) / wgs;
+    long long parts = (256 + wgs - 1) / wgs;
     if (parts > rep) parts = rep;
     // parts of the same number of heads, none of them empty
     const long long each = (rep + parts - 1) / parts;
