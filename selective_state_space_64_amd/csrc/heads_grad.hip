@@ -179,38 +179,18 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
         const In<T> fc[2] = {tile_row<T, NCH>(tC, 32 * ih + r, 4 * b + g), tile_row<T, NCH>(tC, 32 * ih + 16 + r, 4 * b + g)};
         mma_left<2>(M, fc, tile_row<T, NCH>(tB, 16 * jt + r, 4 * b + g));
     }
-    // C and B of the wave's columns n in the rows of its sums (bf16: in pairs), for all heads
-    constexpr bool kHeld = ND <= 128;
-    constexpr int kWords = sizeof(T) == 2 ? 2 * MT : 4 * MT;
-    uint32_t Cn[kHeld ? kWords : 1], Bn[kHeld ? kWords : 1];
-    auto bits_at = [&](const E<T> *tile, int t, int m, int e) {
+    // an element of B or C in the place of a sum (held in registers they cost spills)
+    auto value = [&](const E<T> *tile, int r, int g, int t, int m, int e) {
         const int n = n0 + 16 * t + r, at = chunk_at<NCH>(16 * (m0 + m) + 4 * g + e, n >> 3) + (n & 7);
-        if constexpr (sizeof(T) == 4) return __float_as_uint(tile[at]);
-        else return uint32_t(tile[at]);
-    };
-    if constexpr (kHeld)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * m + e;
-                const uint32_t cv = bits_at(tC, 0, m, e), bv = bits_at(tB, 0, m, e);
-                if constexpr (sizeof(T) == 4) {
-                    Cn[i] = cv;
-                    Bn[i] = bv;
-                } else {
-                    Cn[i / 2] = i % 2 ? Cn[i / 2] | cv << 16 : cv;
-                    Bn[i / 2] = i % 2 ? Bn[i / 2] | bv << 16 : bv;
-                }
-            }
-    auto value = [&](const uint32_t *held, const E<T> *tile, int t, int m, int e) {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(kHeld ? held[4 * m + e] : bits_at(tile, t, m, e));
-        else if constexpr (kHeld) return e % 2 ? io<bf16_t>::hi(held[(4 * m + e) / 2]) : io<bf16_t>::lo(held[(4 * m + e) / 2]);
-        else return io<bf16_t>::lo(bits_at(tile, t, m, e));
+        if constexpr (sizeof(T) == 4) return tile[at];
+        else return io<bf16_t>::lo(tile[at]);
     };
 
     // Head k's step sizes, once its sums are there (one wave, lane = step).
     auto finish = [&](int k) {
+        uint32_t lane = l;  // (its masks and addresses are not kept from before the loop)
+        opaque(lane);
+        const int l = int(lane);
         const int head = h0 + k, q = k & 1;
         const HeadVec &v = vecs[k & (2 * kAhead - 1)];
         float row = 0.0f, E0 = 0.0f, dot = 0.0f;
@@ -249,6 +229,9 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
     // would be waited for where the branch ends)
     RawStep raw;
     auto load_raw = [&](int k) {
+        uint32_t lane = l;
+        opaque(lane);
+        const int l = int(lane);
         const int head = h0 + min(k + (wave & (kAhead - 1)), nh - 1);
         raw.load(in_at(p.dt, p.sdt, head, ein), min(l, rows - 1) * p.sdt.t, p.in_bf16);
     };
@@ -296,6 +279,9 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
         // rows 16 (m0 + m) + 4 g + e, columns n: e^G S0 dy to dC and to row, t dS1 x to dB and to end
         // (the state as an operand first, and the next one's on its way in its place)
         auto side = [&](const E<T> *tile, f32x4 (*state)[NB][2], const float *from, const float *scales, bool isC) {
+            uint32_t lane = l;
+            opaque(lane);
+            const int r = int(lane) & 15, g = int(lane) >> 4;
             Sum<T, NR> f[NT][NB];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -336,10 +322,10 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
                         const float a = scale[e] * acc[m][e];
                         if (isC) {
                             dC[t][m][e] += a;
-                            part[4 * m + e] = __builtin_fmaf(value(Cn, tC, t, m, e), a, part[4 * m + e]);
+                            part[4 * m + e] = __builtin_fmaf(value(tC, r, g, t, m, e), a, part[4 * m + e]);
                         } else {
                             dB[t][m][e] = __builtin_fmaf(dts[e], a, dB[t][m][e]);
-                            part[4 * m + e] = __builtin_fmaf(value(Bn, tB, t, m, e), a, part[4 * m + e]);
+                            part[4 * m + e] = __builtin_fmaf(value(tB, r, g, t, m, e), a, part[4 * m + e]);
                         }
                     }
                 }
@@ -358,6 +344,9 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
         side(tX, d1, p.ws.dS1, v.tail, false);
         if (done) {
             // dW: rows i = 16 (2 ih + m) + 4 g + e, column j = 16 jt + r
+            uint32_t lane = l;
+            opaque(lane);
+            const int r = int(lane) & 15, g = int(lane) >> 4, l = int(lane);
             const int j = 16 * jt + r, q = k & 1;
             const float jhi = v.hi[j], jlo = v.lo[j], jdt = v.dt[j];
             float sums[16], col = 0.0f;
