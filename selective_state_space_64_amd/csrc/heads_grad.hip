@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
     static_assert(2 * 64 * PB >= 8 * kFrag, "Q's fragments take the place of x and dy");
     __shared__ __align__(16) HeadVec vecs[2 * kAhead];
     __shared__ float rows_[2][kGradWaves][16 * MT], ends_[2][kGradWaves][16 * MT], rowsR_[2][kGradWaves][32], cols_[2][2][64],
-        diag_[2][64], diagR_[2][64], dots_[2][kGradWaves];
+        diag_[2][64], diagR_[2][64], dots_[2][kGradWaves], rates[2 * kAhead];  // rates: the heads' A
 
     const int l = int(threadIdx.x) & 63, wave = wave_of(), r = l & 15, g = l >> 4;
     const int jt = wave & 3, ih = wave >> 2;  // the wave's column tile, and half of the row tiles, of the scores
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
             row += (w >> 2) == (l >> 5) ? rowsR_[q][w][l & 31] : 0.0f;
             if (MT == 4 || w < 4) dot += dots_[q][w];  // (MT = 2: the others hold the same states)
         }
-        const float dt = v.dt[l], later = cols_[q][0][l] + cols_[q][1][l] + E0, dD = later + diagR_[q][l], A = p.A[head];
+        const float dt = v.dt[l], later = cols_[q][0][l] + cols_[q][1][l] + E0, dD = later + diagR_[q][l], A = rates[k & (2 * kAhead - 1)];
         const float end = v.up[63];
         // the sums run in double: neighbours cancel
         const double dG = double(row) - double(dt) * later;
@@ -225,25 +225,28 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
     f32x4 dW[2];
     float dot = 0.0f;
     int k = 0, pb = 0;
-    // the raw steps of one of the next four heads (loaded at every step: a load in a branch
-    // would be waited for where the branch ends)
+    // the raw steps of one of the next four heads, its A and dt_bias (loaded at every step: a
+    // load in a branch would be waited for where the branch ends)
     RawStep raw;
+    float rate, bias;
+    const float *const biases = p.bias ? p.bias : p.A;
     auto load_raw = [&](int k) {
         uint32_t lane = l;
         opaque(lane);
         const int l = int(lane);
         const int head = h0 + min(k + (wave & (kAhead - 1)), nh - 1);
         raw.load(in_at(p.dt, p.sdt, head, ein), min(l, rows - 1) * p.sdt.t, p.in_bf16);
+        rate = p.A[head];
+        bias = biases[head];
     };
     load_raw(0);
     const int steps = nh * blocks;
     for (int step = 0; step < steps; ++step) {
-        const int head = h0 + k;
         if (pb == 0) {
             // four heads' decays at a time, a wave each
             if ((k & (kAhead - 1)) == 0 && wave < kAhead && k + wave < nh) {
-                const int mine = head + wave;
-                const Decays d = decays(raw.value(p.in_bf16), p.bias ? p.bias[mine] : 0.0f, p.A[mine], rows);
+                const Decays d = decays(raw.value(p.in_bf16), p.bias ? bias : 0.0f, rate, rows);
+                if (l == 0) rates[(k + wave) & (2 * kAhead - 1)] = rate;
                 HeadVec &v = vecs[(k + wave) & (2 * kAhead - 1)];
                 v.hi[l] = float(d.G);
                 v.lo[l] = float(d.G - double(float(d.G)));
