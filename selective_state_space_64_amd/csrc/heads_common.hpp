@@ -303,24 +303,36 @@ __device__ inline float load_step(const void *p, long long at, int bf16)
 // ---------------------------------------------------------------- workspace
 inline int heads_nd(int N) { return N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
-// Sequence split (as delta_split): where heads x sequences x column tiles leave
-// compute units without a workgroup, a sequence is cut into segments.  All but a
-// sequence's last (in the direction of the run) first yield their end state from
-// zero; composed with the segments' decays, which are numbers here, these give
-// the states that the segments enter with, and all segments run at once.
+// Sequence split: where heads x sequences x column tiles leave compute units without
+// work, a sequence is cut into segments.  All but a sequence's last (in the direction of
+// the run) first yield their end state from zero, by the recurrence without its
+// outputs; composed with the segments' decays, which are numbers here, these give the
+// states that the segments enter with, and all segments run at once.
+//
+// Segments fill the card twice (512 workgroups), which is as many as it holds.  A
+// sequence is cut into three at least: two halves cost as much as they gain.  Measured,
+// N = 128, P = 64, bf16, cut against whole: 24 heads of 65521 steps 321 against 2426 us (400
+// for 256 workgroups, 352 for 1024), 4 sequences of 24 heads of 2048 59 against 84, 80
+// heads of 4096 81 against 160, 24 of 768 28 against 36; below the rule, 8 sequences of 24
+// heads of 2048 105 cut in two against 84, 2 of 80 heads of 1024 52 against 45.  Two
+// chunks a segment at least: 12 heads x 2 of 777 steps in fp32 31 us, with four 42.
+// A packed batch is judged as if one sequence were all of it.
 struct HeadsSplit {
     int seg_chunks, segs;  // segs: an upper bound over all sequences
 };
+constexpr long long kFill = 512, kSegments = 3, kMinSeg = 2;
 inline HeadsSplit heads_split(int batch, int seqlen, int h, int P, int num_seqs)
 {
     const long long chunks = delta_chunks(batch, seqlen, num_seqs), nseq = num_seqs ? num_seqs : batch;
     const long long wgs = (long long)h * ((P + kCols - 1) / kCols);
     const long long per = num_seqs ? chunks : chunks / batch;  // of the longest sequence
-    if ((num_seqs ? 1 : nseq) * wgs > 256) return {0, 0};
-    const long long want = (512 + wgs - 1) / wgs;  // segments in all
+    if (kSegments * (num_seqs ? 1 : nseq) * wgs > kFill) return {0, 0};
+    // segments in all; of packed sequences about half of the last ones are short
+    long long want = kFill / wgs - num_seqs * 5 / 8;
+    if (want < kSegments) want = kSegments;
     long long seg = (chunks + want - 1) / want;
-    if (seg < 4) seg = 4;
-    if (per <= 2 * seg) return {0, 0};
+    if (seg < kMinSeg) seg = kMinSeg;
+    if (per < kSegments * seg) return {0, 0};
     const long long segs = num_seqs ? chunks / seg + num_seqs : batch * ((per + seg - 1) / seg);
     return {int(seg), int(segs)};
 }

@@ -453,15 +453,28 @@ __global__ __launch_bounds__(kThreads) void heads_compose_kernel(const HeadsScan
     if (i >= p.ws.state) return;
     auto at = [&](int k) { return (z0 + (reverse ? segs - 1 - k : k)) * p.h + head; };
     auto place = [&](int k) { return reinterpret_cast<f32x4 *>(p.ws.ends + at(k) * p.ws.state + i); };
-    if (segs < 2) return;
+    if (segs < 3) return;
     f32x4 s = *place(0);
-    for (int k = 1; k + 1 < segs; ++k) {
-        const f32x4 end = *place(k);
-        const float d = p.ws.decay[at(k)];
+    constexpr int kDeep = 4;  // loads under way
+    f32x4 ends[kDeep];
+    float d[kDeep];
+    auto load = [&](int k, int i) {
+        k = min(k, segs - 2);
+        ends[i] = *place(k);
+        d[i] = p.ws.decay[at(k)];
+    };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(d, s[e], end[e]);
-        *place(k) = s;
-    }
+    for (int i = 0; i < kDeep; ++i) load(1 + i, i);
+    for (int k = 1; k + 1 < segs; k += kDeep)
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            if (k + i + 1 < segs) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(d[i], s[e], ends[i][e]);
+                load(k + i + kDeep, i);
+                *place(k + i) = s;
+            }
+        }
 }
 
 template <typename T, int ND, bool kRev, bool kFast>
