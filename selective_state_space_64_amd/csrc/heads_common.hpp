@@ -288,6 +288,7 @@ struct RawStep {
         lo = *reinterpret_cast<const uint16_t *>(q);
         hi = *reinterpret_cast<const uint16_t *>(q + (bf16 ? 0 : 2));
     }
+    __device__ inline void pin() { asm volatile("" : "+v"(lo), "+v"(hi)); }  // waits for it
     __device__ inline float value(int bf16) const
     {
         return __uint_as_float(bf16 ? uint32_t(lo) << 16 : uint32_t(hi) << 16 | lo);

@@ -111,14 +111,18 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
         return off;
     };
     auto record_row = [&](int m, int e) { return uint32_t((32 * (m / 2) + 4 * (m % 2) + e) * p.ws.Pp) * 4u; };
-    auto keep_state = [&](float *to) {
+    auto keep_rows = [&](float *to, int b) {  // 32 b and the 31 behind
         const auto buf = buffer_of(to, p.ws.state * 4);
         const uint32_t off = record_off();
 #pragma unroll
-        for (int m = 0; m < ND / 16; ++m)
+        for (int m = 2 * b; m < 2 * b + 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][e]), buf, off + record_row(m, e), 0, 0);
+    };
+    auto keep_state = [&](float *to) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) keep_rows(to, b);
     };
     auto load_state = [&](const float *from) {
         const auto buf = buffer_of(from, p.ws.state * 4);
@@ -209,6 +213,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
         store(rows_of(0));
         __syncthreads();
     }
+    // What is still on its way is waited for here: a wait in the loop would be one for the
+    // stores of the chunk before as well.
+    raw.pin();
+#pragma unroll
+    for (int m = 0; m < ND / 16; ++m) asm volatile("" : "+v"(S[m]));
 
     // All chunks, as the wave that is the W-th.  Each phase's fragments are read while the
     // phase before it computes, and the vector work (terms, decays) takes turns with matrix
@@ -272,6 +281,11 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
                     }
                     // (the tiles of the triangle: from the diagonal's on, or up to it)
                     constexpr int m0 = kRev ? 0 : W, kTiles = kRev ? W + 1 : 4 - W;
+                    // Kept a part at a time, between the products: a compute unit's stores take about
+                    // 16 bytes a cycle, and a wave that has 32 of them to give waits for that (the
+                    // layer's training step 716 us with all of them in front of the state's update,
+                    // 671 so; rows on their way ahead of them cost registers: 691).
+                    if constexpr (kKeep) keep_rows(pK, b);
                     mma_right<kTiles>(w + m0, fr[b & 1], fl[b & 1] + m0);
                     mma_right<4>(y, fs[b & 1], fl[b & 1]);
                     // the last two have the time to form the operands of the next phase
@@ -283,11 +297,9 @@ __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) vo
                 enter(0);
                 enter(1);
             }
-            // The next chunk's rows on their way, ahead of the stores: what waits for them does
-            // not wait for those.
-            fetch(next_rows);
+            fetch(next_rows);  // the next chunk's, on their way
             if constexpr (kKeep) {
-                keep_state(pK);
+                if constexpr (!kOut) keep_state(pK);
                 pK += dK;
             }
             // S = e^{Gc} S + R^T (scaled v);  beside it W's decays
