@@ -10,7 +10,7 @@
 // row is read once and waits for one sum over the workgroup.  Each input is read
 // once and each output written once: the calls are bound by HBM bandwidth.
 //
-// A row is held in registers by one wave (up to 2048 channels) or by a
+// A row is held in registers by one wave (up to 512 channels) or by a
 // workgroup of just as many waves as it takes; a thread keeps the same channels
 // from row to row, so that the weight stays in registers and dw is summed there,
 // written once a thread, and added in a fixed order by a second small kernel.
@@ -415,7 +415,12 @@ __global__ __launch_bounds__(1024) void rms_sums_kernel(const float *pw, int spl
 
 // ------------------------------------------------------------ launches
 // How a row is held: CH runs by each of `threads` threads (0: read twice), or by
-// a wave of a workgroup of four rows.
+// a wave of a workgroup of four rows.  A wave takes rows of up to 512 channels;
+// longer ones fare better with more waves, which have less to load each (bf16 x, fp32
+// residual, 21 M elements, the wave's limit at 2048 against 512: 64 against 52 us
+// forward and 84 against 75 back at 2048; rows at odd addresses, 1024 against 512: 105
+// against 87 at 1024, and at 512 a workgroup takes 90 where a wave takes 70).  Rows read
+// twice are those that registers do not hold: at 2560 channels held ones take 59 against 104.
 struct Shape {
     int ch, threads;
     bool wave;
@@ -423,20 +428,32 @@ struct Shape {
 Shape rms_shape(int n, bool vec)
 {
     const int run = vec ? 8 : 2, runs = (n + run - 1) / run;
-    if (vec && runs <= 4 * 64) return {runs <= 64 ? 1 : runs <= 2 * 64 ? 2 : 4, 64, true};
-    if (!vec && n <= 8 * 128) return {8, 64, true};
+    if (n <= 512) return {vec ? 1 : 4, 64, true};
     const int waves = vec ? (runs + 63) / 64 : (n + 127) / 128, most = vec ? 2 : 4;
     if (waves <= 16) return {1, 64 * waves, false};
     if (waves <= 16 * most) return {most, 64 * ((waves + most - 1) / most), false};
     return {0, kMaxThreads, false};
 }
 
-// Rows in work at once: enough threads to fill the chip; for the gradients few
-// enough that dw's partial rows stay small beside the tensors.
-unsigned rms_splits(long long rows, int n, bool bwd)
+// Rows in work at once.  Forward: several times what the chip holds, since the next
+// workgroups' loads then overlap the last one's stores (2560 channels: 59 us for 2^22 / n
+// rows, 51 for twice and 50 for four times as many; short rows gain nothing).
+// Gradients: few, so that dw's partial rows stay small beside the tensors, but every
+// compute unit one (16-byte accesses, 2^20 / n against 2^21 / n: 80 against 86 us at 2560
+// channels, 74 against 81 at 512; 8192: 104 for 128 rows, 77 for 256).  Narrow accesses
+// leave more loads to a row: 2^21 / n.
+unsigned rms_splits(long long rows, int n, bool bwd, bool vec)
 {
-    const long long want = (bwd ? 1ll << 21 : 1ll << 22) / n;
-    return unsigned(want < 1 ? 1 : want < rows ? want : rows);
+    long long want;
+    if (bwd) {
+        const long long few = (rows + 1) / 2 < 256 ? (rows + 1) / 2 : 256;
+        want = (vec ? 1ll << 20 : 1ll << 21) / n;
+        if (want < few) want = few;
+    } else {
+        want = (1ll << 24) / n;
+        if (want > 1 << 15) want = 1 << 15;
+    }
+    return unsigned(want < rows ? want : rows);
 }
 
 template <int CH> using Ch = std::integral_constant<int, CH>;
@@ -444,9 +461,9 @@ template <typename F> hipError_t by_shape(const Shape &s, bool vec, F &&f)
 {
     const std::true_type yes;
     const std::false_type no;
-    if (vec && s.wave) return s.ch == 1 ? f(yes, Ch<1>{}, yes) : s.ch == 2 ? f(yes, Ch<2>{}, yes) : f(yes, Ch<4>{}, yes);
+    if (vec && s.wave) return f(yes, Ch<1>{}, yes);
     if (vec) return s.ch == 1 ? f(yes, Ch<1>{}, no) : s.ch == 2 ? f(yes, Ch<2>{}, no) : f(yes, Ch<0>{}, no);
-    if (s.wave) return f(no, Ch<8>{}, yes);
+    if (s.wave) return f(no, Ch<4>{}, yes);
     return s.ch == 1 ? f(no, Ch<1>{}, no) : s.ch == 4 ? f(no, Ch<4>{}, no) : f(no, Ch<0>{}, no);
 }
 
@@ -454,7 +471,7 @@ template <typename T, typename S, typename TOut>
 hipError_t launch_fwd(RmsParams p, bool vec, hipStream_t stream)
 {
     const Shape s = rms_shape(p.n, vec);
-    p.splits = rms_splits(p.rows, p.n, false);
+    p.splits = rms_splits(p.rows, p.n, false, vec);
     return by_shape(s, vec, [&](auto v, auto ch, auto wave) {
         constexpr bool kVec = decltype(v)::value, kWave = decltype(wave)::value;
         constexpr int CH = decltype(ch)::value;
@@ -473,7 +490,7 @@ hipError_t launch_fwd(RmsParams p, bool vec, hipStream_t stream)
 template <typename S, typename G> hipError_t launch_bwd(RmsParams p, bool vec, hipStream_t stream)
 {
     const Shape s = rms_shape(p.n, vec);
-    p.splits = rms_splits(p.rows, p.n, true);
+    p.splits = rms_splits(p.rows, p.n, true, vec);
     return by_shape(s, vec, [&](auto v, auto ch, auto wave) {
         constexpr bool kVec = decltype(v)::value, kWave = decltype(wave)::value;
         constexpr int CH = decltype(ch)::value;
@@ -603,7 +620,7 @@ ssm_status_t ssm_rms_norm_fwd(int batch, int seqlen, int dim, ssm_dtype_t in_dty
 size_t ssm_rms_norm_bwd_workspace_bytes(int batch, int seqlen, int dim)
 {
     if (!ssm::rms_sizes(batch, seqlen, dim)) return 0;
-    return sizeof(float) * size_t(dim) * size_t(ssm::rms_splits((long long)batch * seqlen, dim, true));
+    return sizeof(float) * size_t(dim) * size_t(ssm::rms_splits((long long)batch * seqlen, dim, true, false));  // (the larger)
 }
 
 ssm_status_t ssm_rms_norm_bwd(int batch, int seqlen, int dim, ssm_dtype_t stream_dtype, ssm_dtype_t grad_dtype,
@@ -662,7 +679,7 @@ ssm_status_t ssm_rms_norm_bwd(int batch, int seqlen, int dim, ssm_dtype_t stream
                                    : (g_t == SSM_BF16 ? launch_bwd<float, bf16_t>(p, vec, s)
                                                       : launch_bwd<float, float>(p, vec, s));
     if (e == hipSuccess && dweight) {
-        rms_sums_kernel<<<dim3((dim + 31) / 32), dim3(1024), 0, s>>>(p.pw, int(rms_splits(p.rows, dim, true)), dim,
+        rms_sums_kernel<<<dim3((dim + 31) / 32), dim3(1024), 0, s>>>(p.pw, int(rms_splits(p.rows, dim, true, vec)), dim,
                                                                      dweight);
         e = hipGetLastError();
     }
