@@ -312,7 +312,7 @@ inline int heads_nd(int N) { return N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 //
 // Segments fill the card twice (512 workgroups), which is as many as it holds.  A
 // sequence is cut into three at least: two halves cost as much as they gain.  Measured,
-// N = 128, P = 64, bf16, cut against whole: 24 heads of 65521 steps 321 against 2426 us (400
+// N = 128, P = 64, bf16, cut against whole: 24 heads of 65521 steps 329 against 2426 us (400
 // for 256 workgroups, 352 for 1024), 4 sequences of 24 heads of 2048 59 against 84, 80
 // heads of 4096 81 against 160, 24 of 768 28 against 36; below the rule, 8 sequences of 24
 // heads of 2048 105 cut in two against 84, 2 of 80 heads of 1024 52 against 45.  Two

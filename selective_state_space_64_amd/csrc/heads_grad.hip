@@ -17,6 +17,12 @@
 // and dDskip is the sum of dW's diagonal.  (R's diagonal does not depend on G:
 // left in both sums of dG it would cancel up to roundings, which are all that is
 // left of dA where the decays are strong.)
+//
+// What bounds it (4 x 2048 steps, 80 heads of 128 x 64 with one group, bf16): the states.  They
+// are 671 MB of the 860 MB read, 165 us at a large copy's rate; the kernel takes 282,
+// one workgroup of eight waves on every compute unit (the registers hold no second one),
+// and the two runs that write them 212 and 215 (all under the profiler) where a forward
+// call without them takes 126.  The whole training step takes 671 us (parts and sums 14).
 #include "heads_common.hpp"
 
 namespace ssm {

@@ -8,7 +8,8 @@
 // state and all N rows: a thread 4 neighbouring columns of every 256 /
 // (tile / 4)-th row.  An element is stored as soon as it is updated; only y waits
 // for the sum over N, which goes through lane moves inside a wave and LDS across
-// the four.
+// the four.  64 sequences of 80 heads of 128 x 64: 61.6 us, 5.5 TB/s; one sequence 4 us of
+// kernel in a call of 12.
 #include "heads_launch.hpp"
 #include "ssm_device.hpp"
 #include "ssm_launch.hpp"
