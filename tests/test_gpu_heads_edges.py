@@ -292,6 +292,30 @@ def test_optional_outputs():
         assert torch.equal(d1[n], d2[n]), n
 
 
+@pytest.mark.parametrize("lens,packed", [([130, 130], False), ([1500], False), ([700, 0, 900, 65], True)])
+def test_checkpoints_stay(lens, packed):
+    """Two backward calls on one workspace that the forward call filled."""
+    t, _, cu = make(BF16, lens, packed, 1, 2, 64, 40, seed=16)
+    ws = ssm.ssm_head_scan_bwd_workspace(t["x"], t["B"], cu_seqlens=cu)
+    call(t, cu, checkpoints=ws)
+    first, second = (call_bwd(t, cu, workspace=ws, checkpoints_in_workspace=True) for _ in range(2))
+    for n in first:
+        assert torch.equal(first[n], second[n]), n
+
+
+@pytest.mark.parametrize("batch,N,P", [(3, 20, 64), (2, 64, 128), (3, 100, 64), (2, 256, 64), (1, 200, 192)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_update_tiles_of_64(dtype, batch, N, P):
+    """The decode step's wide tiles for every number of state rows, and what lies beside a state."""
+    t, r, _ = make(dtype, [1] * batch, False, 2, 4, N, P, seed=N)
+    y0, h0 = reference(r)
+    pool = torch.full((batch + 2, 4, N, P), 7.0, device="cuda")
+    pool[1:-1].copy_(t["h0"])
+    y = ssm.ssm_head_scan_update(pool[1:-1], *steps(t, 0), Dskip=t["D"], dt_bias=t["bias"])
+    assert error(y, y0[:, 0]) <= tolerance(F32, dtype) and error(pool[1:-1], h0) <= tolerance(F32, F32)
+    assert (pool[0] == 7).all() and (pool[-1] == 7).all()
+
+
 def test_stream_and_graph():
     """On another stream than the inputs', and captured: every replay gives the eager bits."""
     lens = [130, 0, 65, 1, 700]

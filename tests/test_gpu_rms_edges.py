@@ -243,3 +243,25 @@ def test_stream_and_graph():
         for got, want in zip([*out, res], ref):
             assert torch.equal(got, want)
         torch.randn(64, 64, device="cuda").sum().item()
+
+
+@pytest.mark.parametrize("rows,dim", [(2600, 9001), (1500, 16392), (1100, 20001), (40000, 512), (40000, 99)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_several_rows_a_workgroup(rows, dim, dtype):
+    """More rows than are in work at once, for every way that a row is held."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x, dy, dh, res = (torch.randn(rows, dim, device="cuda", generator=g).to(dtype) for _ in range(4))
+    w = 1 + 0.1 * torch.randn(dim, device="cuda", generator=g)
+    y, h, _ = ssm.ssm_rms_norm_fwd(x, weight=w, residual=res)
+    d = ssm.ssm_rms_norm_bwd(h, dy, weight=w, dh=dh)
+
+    def off(got, ref):
+        size = torch.maximum(ref.abs(), ref.square().mean().sqrt())
+        return float(((got.double() - ref).abs() / size).max())
+    s = x.double() + res.double()
+    assert off(y, s * (s.square().mean(-1, keepdim=True) + 1e-5).rsqrt() * w) <= tolerance(dtype)
+    h, u = h.double(), dy.double() * w
+    r = (h.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    assert off(d["dx"], r * (u - h * r * r * (u * h).mean(-1, keepdim=True)) + dh.double()) <= tolerance(dtype)
+    # a sum of 4e4 rows in fp32: the threads' own chains of up to 40 rows, then a tree
+    assert off(d["dweight"], (dy.double() * h * r).sum(0)) <= FP32_ERROR
