@@ -248,7 +248,6 @@ __device__ inline double from_lane(double v, int lane)
 // Lane t of a wave has step t; G in units of log2.
 struct Decays {
     float dt;    // softplus(dt + bias), 0 behind the last row
-    float u;     // dt + bias
     double G;    // sum of the decays up to the step
     double end;  // of all 64
 };
@@ -256,8 +255,7 @@ __device__ inline Decays decays(float raw, float bias, float A, int rows)
 {
     Decays d;
     const bool live = int(threadIdx.x & 63) < rows;
-    d.u = raw + bias;
-    d.dt = live ? softplus(d.u) : 0.0f;
+    d.dt = live ? softplus(raw + bias) : 0.0f;
     // a decay of e^-110 is 0 in fp32; clamped, it does not cost later steps'
     // differences their low bits (a NaN stays one)
     const double a = double(d.dt) * double(A);
@@ -294,12 +292,6 @@ struct RawStep {
         return __uint_as_float(bf16 ? uint32_t(lo) << 16 : uint32_t(hi) << 16 | lo);
     }
 };
-__device__ inline float load_step(const void *p, long long at, int bf16)
-{
-    RawStep raw;
-    raw.load(p, at, bf16);
-    return raw.value(bf16);
-}
 
 // ---------------------------------------------------------------- workspace
 inline int heads_nd(int N) { return N <= 64 ? 64 : N <= 128 ? 128 : 256; }
