@@ -248,8 +248,10 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
     load_raw(0);
     const int steps = nh * blocks;
     for (int step = 0; step < steps; ++step) {
+        __syncthreads();  // the last tiles' reads are done, and the finishing wave's of its head's decays
         if (pb == 0) {
-            // four heads' decays at a time, a wave each
+            // four heads' decays at a time, a wave each (behind the barrier: with kAhead = 1 and one
+            // block of columns a head they take the place of those that finish() read last)
             if ((k & (kAhead - 1)) == 0 && wave < kAhead && k + wave < nh) {
                 const Decays d = decays(raw.value(p.in_bf16), p.bias ? bias : 0.0f, rate, rows);
                 if (l == 0) rates[(k + wave) & (2 * kAhead - 1)] = rate;
@@ -265,7 +267,6 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
             dot = 0.0f;
         }
         const HeadVec &v = vecs[k & (2 * kAhead - 1)];
-        __syncthreads();  // the last tiles' reads are done
         E<T> *const tX = tXY, *const tY = tXY + 64 * PB;
         inX.store(tX, x_at(k, pb), p.sx.t, rows, p.P - pb * PB, p.in_bf16);
         inY.store(tY, y_at(k, pb), p.sdy.t, rows, p.P - pb * PB, p.g_bf16);
