@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradPara
     const DeltaSeq seq = delta_seq(p.cu, si, p.seqlen);
     const int c = record - seq.chunk0, left = seq.len - c * kDeltaChunk;
     auto sum_at = [&](int which, int head) { return (which * (long long)p.h + head) * p.records + record; };
-    if (left <= 0) {  // no such chunk
+    if (c < 0 || left <= 0) {  // no such chunk: records in front of the first sequence, or behind one's last
         for (int k = int(threadIdx.x); k < nh; k += kGradThreads)
             for (int i = 0; i < 3; ++i) p.ws.sums[sum_at(i, h0 + k)] = 0.0f;
         return;
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kThreads) void heads_parts_kernel(const GradParams 
     const int record = int(blockIdx.x), group = int(blockIdx.y);
     const DeltaSeq seq = delta_seq(p.cu, delta_seq_of(p.cu, p.nseq, p.seqlen, record), p.seqlen);
     const int c = record - seq.chunk0, left = seq.len - c * kDeltaChunk;
-    if (left <= 0) return;
+    if (c < 0 || left <= 0) return;
     const bool isC = blockIdx.z != 0;
     const DeltaStride &s = isC ? p.sdC : p.sdB;
     const float *src = (isC ? p.ws.dCp : p.ws.dBp) + ((long long)record * p.groups + group) * 64 * p.ws.Nr;

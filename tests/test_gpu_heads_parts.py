@@ -1,7 +1,9 @@
 """Gradients of the head scan where a workgroup goes through many heads of a
 chunk, all of them live: the heads' decays, sums and rows take turns in the same
-places from head to head, and dB and dC add up over them.  Tolerances are those
-of test_gpu_heads (derived there)."""
+places from head to head, and dB and dC add up over them; and what the records
+that no sequence has leave alone.  Tolerances are those of test_gpu_heads (derived
+there)."""
+import numpy as np
 import pytest
 import torch
 
@@ -65,3 +67,27 @@ def test_heads_of_a_part(dtype, grad, N, P, seqs, each):
     for n in d0:
         assert torch.equal(d[n], e[n]), n
         assert error(d[n], d0[n]) <= tolerance(dtype, d[n].dtype, n), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L,cu,g", [(300, [130, 170, 240], 1), (300, [130, 170, 240], 2), (200, [64, 64, 199], 1),
+                                    (1500, [700, 1450], 1), (1500, [250, 1400, 1400, 1499], 2)])
+def test_steps_in_front_of_the_first_sequence(L, cu, g, dtype):
+    """Bounds that begin behind the first chunk: the steps in front keep what the
+    outputs held, and nothing of them is in the sums."""
+    h, N, P = 2, 32, 16
+    t, r, _ = make(dtype, [L], False, g, h, N, P, seed=L, state=False)
+    bounds = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    held = lambda *shape: torch.full((1, L, *shape), 7.0, device="cuda", dtype=dtype)  # noqa: E731
+    out = {"dx": held(h, P), "ddt": held(h), "dBm": held(g, N), "dCm": held(g, N)}
+    y, hL = call(t, bounds, y=held(h, P))
+    d = call_bwd(t, bounds, **out)
+    inside = {n: v[:, cu[0]:cu[-1]] if n in ("x", "dt", "B", "C", "dy") else v for n, v in r.items()}
+    inside["dhL"] = np.zeros((len(cu) - 1, h, N, P))
+    y0, h0, d0 = reference(inside, list(np.diff(cu)), grads=True)
+    assert error(hL, h0) <= tolerance(dtype, F32, "hL")
+    for n, got, want in [("y", y, y0)] + [(n, d[n], d0[n]) for n in d0]:
+        if n == "y" or n in out:
+            assert (got[:, :cu[0]] == 7.0).all() and (got[:, cu[-1]:] == 7.0).all(), n
+            got = got[:, cu[0]:cu[-1]]
+        assert error(got, want) <= tolerance(dtype, got.dtype, n), n
