@@ -35,9 +35,9 @@
  *     Products run on the matrix cores.  Where all tensors of a call are bf16
  *     (out_dtype and grad_dtype aside: see there), operands that are not exact
  *     in bf16 are split into bf16 terms: three (24 bits of significand) where
- *     they enter a state, two (16 bits) in what forms y, dx, dB and dC, under the
- *     rounding of a bf16 output; an fp32 y of bf16 inputs has relative errors of
- *     about 4e-6 (errors of fp32 arithmetic for a caller who passes the same
+ *     they enter a state or form an fp32 y, two (16 bits) in what forms a bf16
+ *     y, dx, dB and dC, 256 times under those outputs' own rounding (errors of
+ *     fp32 arithmetic in dx, dB and dC for a caller who passes the same
  *     values as fp32).  Otherwise the products are fp32 ones.  The decode step
  *     computes in fp32 throughout.
  *   - A step's log decay D_t A below -110 acts as -110 (e^-110 is 0 in fp32).

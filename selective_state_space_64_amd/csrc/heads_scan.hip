@@ -71,16 +71,21 @@ __device__ inline void store_out(char *out, long long step, int bf16, int rows, 
     }
 }
 
-template <typename T, int ND, int kRun, bool kRev, bool kFast>
+// NY: terms of W and of the state as the readout sees it (bf16 compute).
+template <typename T, int ND, int kRun, bool kRev, bool kFast, int NY>
 __global__ __launch_bounds__(kThreads, (sizeof(T) == 2 && ND <= 128 ? 2 : 1)) void heads_scan_kernel(const HeadsScan p)
 {
     constexpr bool kOut = kRun == kOutRun || kRun == kOutKeepRun, kKeep = kRun == kOutKeepRun || kRun == kKeepRun,
                    kEnd = kRun == kEndRun;
     constexpr int NCH = ND / 8, KB = ND / 32, kTile = 64 * ND, kVCH = kCols / 8;
-    // Terms of bf16 compute.  W and the state as the readout sees it: two (2^-17 of a
-    // value, under the rounding of a bf16 y); what enters the state: three (2^-25),
-    // since the fp32 states of a whole sequence are sums of it.
-    constexpr int NW = 2, NR = 2, NX = 3;
+    // Terms of bf16 compute.  W and the state as the readout sees it: two under a bf16 y (up to
+    // 2^-17 of a value, 256 times under its rounding: its error is that of fp32 products to four
+    // digits, and single elements next to a tie round the other way), three for an fp32 y (off by
+    // 1e-7 of its size, as fp32 products are; with two by 2.4e-6).  The layer's forward takes
+    // 151 us with an fp32 y, 134 with two terms.  Three under a bf16 y too were measured: 144 us
+    // against 126, packed prompts 138 against 126, the training step 682 against 672.  What
+    // enters the state: three (2^-25), since the fp32 states of a whole sequence are sums of it.
+    constexpr int NW = NY, NR = NY, NX = 3;
     constexpr int kFrag = 512 * (sizeof(T) == 2 ? NW : 1);
     // Chunks whose decays are formed at a time, a wave each; the next ones' while these
     // are in work (fp32 tiles of 256 entries leave LDS for two).
@@ -504,20 +509,26 @@ hipError_t scan_run(const HeadsArgs &a, const HeadsScan &p, hipStream_t stream)
     const HeadsSplit split = heads_split(a.batch, a.seqlen, a.h, a.P, a.cu ? a.nseq : 0);
     const dim3 grid(split.segs ? split.segs : a.nseq, a.h, (a.P + kCols - 1) / kCols), block(kThreads);
     if (log_enabled())
-        log_line("head_scan: heads_scan_kernel<%s, N %d, reverse %d, fast %d>, out %d, keep %d, grid (%u, %u, %u) x %u "
+        log_line("head_scan: heads_scan_kernel<%s, N %d, reverse %d, fast %d>, out %d (%s), keep %d, grid (%u, %u, %u) x %u "
                  "threads, %d chunks a segment", type_tag<T>(), ND, int(kRev), int(kFast), int(p.out != nullptr),
-                 int(p.keep != nullptr), grid.x, grid.y, grid.z, block.x, split.seg_chunks);
+                 p.out_bf16 ? "bf16" : "f32", int(p.keep != nullptr), grid.x, grid.y, grid.z, block.x, split.seg_chunks);
     if (split.segs) {
-        heads_scan_kernel<T, ND, kEndRun, kRev, kFast><<<grid, block, 0, stream>>>(p);
+        heads_scan_kernel<T, ND, kEndRun, kRev, kFast, 2><<<grid, block, 0, stream>>>(p);
         const dim3 parts(a.nseq, a.h, (p.ws.state / 4 + kThreads - 1) / kThreads);
         heads_compose_kernel<<<parts, block, 0, stream>>>(p, kRev);
     }
     if constexpr (kRev) {
-        heads_scan_kernel<T, ND, kOutKeepRun, kRev, kFast><<<grid, block, 0, stream>>>(p);
+        // (bf16 compute has gradients of bf16)
+        heads_scan_kernel<T, ND, kOutKeepRun, kRev, kFast, 2><<<grid, block, 0, stream>>>(p);
     } else {
-        if (p.out && p.keep) heads_scan_kernel<T, ND, kOutKeepRun, kRev, kFast><<<grid, block, 0, stream>>>(p);
-        else if (p.out) heads_scan_kernel<T, ND, kOutRun, kRev, kFast><<<grid, block, 0, stream>>>(p);
-        else heads_scan_kernel<T, ND, kKeepRun, kRev, kFast><<<grid, block, 0, stream>>>(p);
+        auto run = [&](auto terms) {
+            constexpr int NY = decltype(terms)::value;
+            if (p.keep) heads_scan_kernel<T, ND, kOutKeepRun, kRev, kFast, NY><<<grid, block, 0, stream>>>(p);
+            else heads_scan_kernel<T, ND, kOutRun, kRev, kFast, NY><<<grid, block, 0, stream>>>(p);
+        };
+        if (!p.out) heads_scan_kernel<T, ND, kKeepRun, kRev, kFast, 2><<<grid, block, 0, stream>>>(p);
+        else if (p.out_bf16) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, sizeof(T) == 4 ? 2 : 3>{});  // (fp32 compute has no terms)
     }
     return hipGetLastError();
 }
