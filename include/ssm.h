@@ -46,7 +46,8 @@
  *     SSM_ERR_HIP.  Faults inside a kernel surface at the caller's next
  *     synchronisation of `stream`.
  *   - Calls are asynchronous: they return once the work is enqueued on
- *     `stream` (a hipStream_t; NULL is the default stream).
+ *     `stream` (a hipStream_t; NULL is the default stream), which must belong
+ *     to the current device, as the tensors must.
  */
 #ifndef SSM_H
 #define SSM_H

@@ -364,13 +364,21 @@ def _on_caller_stream(fn):
     """Run the call with `stream` (when given) as the current stream, so that
     every tensor allocated inside it (outputs, workspace) belongs to the stream
     the kernels are enqueued on: the caching allocator then cannot hand such a
-    block to work on another stream while these kernels still use it."""
+    block to work on another stream while these kernels still use it.  And with
+    the tensors' device as the current one: the library launches on that."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
+        first = args[0] if args else next((t for t in kw.values() if isinstance(t, torch.Tensor)), None)
+        device = first.get_device() if isinstance(first, torch.Tensor) else -1  # -1: not on a GPU
+        if stream is not None:
+            if device >= 0 and stream.device_index != device:
+                raise ValueError("stream belongs to device %d, the tensors are on device %d" % (stream.device_index, device))
+            with torch.cuda.stream(stream):
+                return fn(*args, stream=stream, **kw)
+        if device < 0 or device == torch.cuda.current_device():
             return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kw)
+        with torch.cuda.device(device):
+            return fn(*args, **kw)
     return call
 
 
@@ -580,7 +588,7 @@ class StateUpdateSteps:
     for every step), each step's slice a batch-strided view as
     ssm_state_update accepts.  The buffers must stay alive and in place while
     the object is used; the stream is fixed at construction (the current one
-    by default).  The library still validates every call."""
+    by default), and its device has to be the current one at every step.  The library still validates every call."""
 
     def __init__(self, state, A, xs, dts, Bs, Cs, *, ys, dt_bias=None, Dskip=None, zs=None,
                  zoh=False, stream=None):
@@ -844,7 +852,7 @@ def ssm_conv1d_update(state, x, weight, *, bias=None, silu=True, out_dtype=None,
     return y
 
 
-# The calls below check their arguments on (shape, strides, dtype, is_cuda) of
+# The calls below check their arguments on (shape, strides, dtype, device) of
 # each tensor, and keep what follows from those alone (sizes, type codes, the
 # layout struct) for later calls with the same ones: a decode step's host time
 # is then the pointers and one C call.  Addresses are never kept.
@@ -852,9 +860,9 @@ _plan = functools.lru_cache(maxsize=512)
 
 
 def _meta(**tensors):
-    """(name, shape, strides, dtype, is_cuda) of each tensor, None where absent."""
+    """(name, shape, strides, dtype, GPU or -1) of each tensor, None where absent."""
     try:
-        return tuple([None if t is None else (n, t.shape, t.stride(), t.dtype, t.is_cuda)
+        return tuple([None if t is None else (n, t.shape, t.stride(), t.dtype, t.get_device())
                       for n, t in tensors.items()])
     except (AttributeError, TypeError):
         raise TypeError("%s must be CUDA (HIP) tensors" % ", ".join(
@@ -893,9 +901,14 @@ def _dense(*wanted):
 
 
 def _on_gpu(*metas):
+    first = None
     for m in metas:
-        if m is not None and not m[4]:
-            raise TypeError("%s must be a CUDA (HIP) tensor" % m[0])
+        if m is not None:
+            if m[4] < 0:
+                raise TypeError("%s must be a CUDA (HIP) tensor" % m[0])
+            first = first or m
+            if m[4] != first[4]:
+                raise ValueError("%s is on device %d, %s on device %d" % (m[0], m[4], first[0], first[4]))
 
 
 def _layout(cls, order, *wanted):
