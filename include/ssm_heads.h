@@ -49,7 +49,9 @@
  *   - Every pointer must be aligned to its element size; the decode `state`
  *     must be 16-byte aligned.
  * Supported sizes: batch, num_seqs and heads <= 65535, groups a divisor of
- * heads, 1 <= N <= 256, 1 <= P <= 65536, 1 <= seqlen <= 2^28 - 4096.
+ * heads, 1 <= N <= 256, 1 <= P <= 65536, 1 <= seqlen <= 2^28 - 4096; for the
+ * gradients and for kept checkpoints less than 2^23 chunks of 64 steps in all
+ * (batch x ceil(seqlen / 64), packed ceil(seqlen / 64) + num_seqs).
  */
 #ifndef SSM_HEADS_H
 #define SSM_HEADS_H

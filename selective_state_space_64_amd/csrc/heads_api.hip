@@ -24,6 +24,13 @@ bool heads_sizes(int batch, int seqlen, int groups, int h, int N, int P, int num
                    (unsigned long long)((N + 31ll) * (P + 31ll)) < ((unsigned __int128)1 << 48);
 }
 
+// The gradients' grid has a workgroup a chunk, and a grid's index less than 2^32
+// work-items: sizes whose states may be kept.
+bool heads_kept_sizes(int batch, int seqlen, int num_seqs)
+{
+    return ssm::delta_chunks(batch, seqlen, num_seqs) < (1ll << 32) / ssm::kHeadsGradThreads;
+}
+
 }  // namespace
 
 extern "C" {
@@ -36,7 +43,7 @@ size_t ssm_head_scan_fwd_workspace_bytes(int batch, int seqlen, int groups, int 
 
 size_t ssm_head_scan_bwd_workspace_bytes(int batch, int seqlen, int groups, int heads, int N, int P, int num_seqs)
 {
-    if (!heads_sizes(batch, seqlen, groups, heads, N, P, num_seqs)) return 0;
+    if (!heads_sizes(batch, seqlen, groups, heads, N, P, num_seqs) || !heads_kept_sizes(batch, seqlen, num_seqs)) return 0;
     return ssm::heads_bwd_workspace_bytes(batch, seqlen, groups, heads, N, P, num_seqs);
 }
 
@@ -52,7 +59,7 @@ ssm_status_t ssm_head_scan_fwd(int batch, int seqlen, int groups, int heads, int
     if (!x || !dt || !A || !Bm || !Cm || !y || (ckpt && !workspace)) return SSM_ERR_NULL_ARG;
     if (!valid_dtype(in_t) || !valid_dtype(out_t)) return SSM_ERR_BAD_DTYPE;
     if (!heads_sizes(batch, seqlen, groups, heads, N, P, num_seqs) || (cu_seqlens && num_seqs < 1) ||
-        (!cu_seqlens && num_seqs != 0))
+        (!cu_seqlens && num_seqs != 0) || (ckpt && !heads_kept_sizes(batch, seqlen, num_seqs)))
         return SSM_ERR_BAD_SHAPE;
     if (flags & ~SSM_FLAG_CHECKPOINTS) return SSM_ERR_UNSUPPORTED;
     const ssm_head_scan_layout_t dense{};
@@ -105,7 +112,7 @@ ssm_status_t ssm_head_scan_bwd(int batch, int seqlen, int groups, int heads, int
         return SSM_ERR_NULL_ARG;
     if (!valid_dtype(in_t) || !valid_dtype(g_t)) return SSM_ERR_BAD_DTYPE;
     if (!heads_sizes(batch, seqlen, groups, heads, N, P, num_seqs) || (cu_seqlens && num_seqs < 1) ||
-        (!cu_seqlens && num_seqs != 0))
+        (!cu_seqlens && num_seqs != 0) || !heads_kept_sizes(batch, seqlen, num_seqs))
         return SSM_ERR_BAD_SHAPE;
     if (flags & ~SSM_FLAG_CHECKPOINTS) return SSM_ERR_UNSUPPORTED;
     const ssm_head_scan_bwd_layout_t dense{};

@@ -90,7 +90,8 @@ __device__ inline float one_minus_exp(float x)
 // tiles i, and the columns n of dB and dC that are its own.  S0 and dS1 are read
 // once, straight from memory to the lanes that need them as operands (8
 // neighbouring columns of P of one n), a block of 64 columns ahead.
-constexpr int kGradWaves = 8, kGradThreads = 64 * kGradWaves;
+constexpr int kGradThreads = kHeadsGradThreads, kGradWaves = kGradThreads / 64;
+static_assert(kGradWaves == 8, "the column tiles and halves below");
 
 template <typename T, int ND, bool kFast>
 __global__ __launch_bounds__(kGradThreads) void heads_grad_kernel(const GradParams p)

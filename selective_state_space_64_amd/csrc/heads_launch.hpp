@@ -43,6 +43,7 @@ struct HeadsUpdateArgs {
 };
 
 constexpr int kHeadsMaxN = 256, kHeadsMaxP = 65536;
+constexpr int kHeadsGradThreads = 512;  // of a workgroup of the gradients
 
 size_t heads_fwd_workspace_bytes(int batch, int seqlen, int groups, int h, int N, int P, int num_seqs);
 size_t heads_bwd_workspace_bytes(int batch, int seqlen, int groups, int h, int N, int P, int num_seqs);
