@@ -302,14 +302,21 @@ inline int heads_nd(int N) { return N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 // outputs; composed with the segments' decays, which are numbers here, these give the
 // states that the segments enter with, and all segments run at once.
 //
-// Segments fill the card twice (512 workgroups), which is as many as it holds.  A
-// sequence is cut into three at least: two halves cost as much as they gain.  Measured,
-// N = 128, P = 64, bf16, cut against whole: 24 heads of 65521 steps 329 against 2426 us (400
-// for 256 workgroups, 352 for 1024), 4 sequences of 24 heads of 2048 59 against 84, 80
-// heads of 4096 81 against 160, 24 of 768 28 against 36; below the rule, 8 sequences of 24
-// heads of 2048 105 cut in two against 84, 2 of 80 heads of 1024 52 against 45.  Two
-// chunks a segment at least: 12 heads x 2 of 777 steps in fp32 31 us, with four 42.
-// A packed batch is judged as if one sequence were all of it.
+// Segments fill the card twice (512 workgroups), which is as many as it holds where the
+// rule was measured: bf16 operands with N <= 128 (and fp32 ones with N <= 64).  Of the
+// other kernels a compute unit holds one workgroup, and 512 run in two rounds: not
+// measured apart.  A sequence is cut into three at least: two halves cost as much as they
+// gain.  Measured, N = 128, P = 64, bf16, cut against whole: 24 heads of 65521 steps 329
+// against 2426 us (400 for 256 workgroups, 352 for 1024), 4 sequences of 24 heads of 2048
+// 59 against 84, 80 heads of 4096 81 against 160, 24 of 768 28 against 36; below the rule,
+// 8 sequences of 24 heads of 2048 105 cut in two against 84, 2 of 80 heads of 1024 52
+// against 45.  Two chunks a segment at least: 12 heads x 2 of 777 steps in fp32 31 us,
+// with four 42.
+// A packed batch is judged as if one sequence were all of it, since the host does not know
+// the lengths.  That suits a long one among short ones; equal ones lose by it: 8 packed
+// sequences of 24 heads of 2048 are cut in two and take 116 us (as batch rows, whole, 81);
+// of 16 of 1024 none is cut, and the run for the ends and the composition find nothing to
+// do (74 against 66).
 struct HeadsSplit {
     int seg_chunks, segs;  // segs: an upper bound over all sequences
 };
@@ -320,7 +327,8 @@ inline HeadsSplit heads_split(int batch, int seqlen, int h, int P, int num_seqs)
     const long long wgs = (long long)h * ((P + kCols - 1) / kCols);
     const long long per = num_seqs ? chunks : chunks / batch;  // of the longest sequence
     if (kSegments * (num_seqs ? 1 : nseq) * wgs > kFill) return {0, 0};
-    // segments in all; of packed sequences about half of the last ones are short
+    // segments in all; of packed sequences the last ones are short (by half of one each, and some
+    // more: the factor was not varied)
     long long want = kFill / wgs - num_seqs * 5 / 8;
     if (want < kSegments) want = kSegments;
     long long seg = (chunks + want - 1) / want;

@@ -22,11 +22,13 @@
 // What bounds it (4 x 2048 steps, 80 heads of 128 x 64 with one group, bf16): the chain of
 // products inside a chunk.  126 us, where the tensors' 184 MB take 35 us at a large copy's
 // rate and the products, split terms and all, 56 us at a large matrix product's; of the
-// time vector ALUs are busy for 54 %, matrix pipes 38 %, LDS 55 %.  320 workgroups leave
-// 192 of the compute units with one, which takes 95 us by itself, and 64 with two: 512
-// workgroups take 153.  Not faster for the same layer (at 132 us then): two waves of 32
-// columns with copies straight to LDS (164), four waves with such copies (139), a third
-// barrier a chunk (150).
+// busy compute units' cycles vector ALUs issue in 41 %, matrix pipes are busy in 31 %, LDS
+// in 44 %.  320 workgroups leave 192 of the compute units with one, which takes 95 us by
+// itself, and 64 with two: 512 workgroups take 153.  Not faster for the same layer (at 132
+// us then): two waves of 32 columns with copies straight to LDS (164), four waves with such
+// copies (139), a third barrier a chunk (150).  fp32 tensors take 564 us.  256 state rows
+// do not fit the registers: 290 us with 104 bytes of scratch a lane in bf16, 2.55 ms with
+// 1072 in fp32.
 #include "heads_common.hpp"
 
 namespace ssm {

@@ -8,8 +8,8 @@
 // state and all N rows: a thread 4 neighbouring columns of every 256 /
 // (tile / 4)-th row.  An element is stored as soon as it is updated; only y waits
 // for the sum over N, which goes through lane moves inside a wave and LDS across
-// the four.  64 sequences of 80 heads of 128 x 64: 61.6 us, 5.5 TB/s; one sequence 4 us of
-// kernel in a call of 12.
+// the four.  64 sequences of 80 heads of 128 x 64, bf16 inputs: 58.1 us, 5.8 TB/s; with their
+// states in a pool of 80 slots 61.3 us, 5.5 TB/s; one sequence 4 us of kernel in a call of 12.
 #include "heads_launch.hpp"
 #include "ssm_device.hpp"
 #include "ssm_launch.hpp"
@@ -142,9 +142,10 @@ hipError_t launch_rows(const HeadsStep &p, int batch, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Tiles of 64 columns where they leave no lane idle, else of 32.  Measured, 80 heads of
-// 128 x 64, 64 sequences, fp32 states: 57.8 us with 64 columns (5.8 TB/s), 60.1 with 32 and
-// 96.8 with 16; one sequence 10.9, 10.8 and 11.2 (the host's call).
+// Tiles of 64 columns where they leave no lane idle, else of 32.  Measured in one
+// run, 80 heads of 128 x 64, bf16 inputs, tiles of 64, 32 and 16 columns: 64 sequences 58.1,
+// 60.0 and 97.6 us (fp32 inputs 54.5, 57.6 and 99.9), in a pool of 80 slots 61.3, 63.5 and
+// 108.3; one sequence 12.0 with each (the host's call).
 template <typename T, typename TOut>
 hipError_t launch_typed(const HeadsStep &p, int batch, bool vec, hipStream_t stream)
 {

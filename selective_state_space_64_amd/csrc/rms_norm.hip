@@ -420,9 +420,10 @@ __global__ __launch_bounds__(1024) void rms_sums_kernel(const float *pw, int spl
 // a wave of a workgroup of four rows.  A wave takes rows of up to 512 channels;
 // longer ones fare better with more waves, which have less to load each (bf16 x, fp32
 // residual, 21 M elements, the wave's limit at 2048 against 512: 64 against 52 us
-// forward and 84 against 75 back at 2048; rows at odd addresses, 1024 against 512: 105
-// against 87 at 1024, and at 512 a workgroup takes 90 where a wave takes 70).  Rows read
-// twice are those that registers do not hold: at 2560 channels held ones take 59 against 104.
+// forward and 84 against 75 back at 2048; rows at odd addresses, back, 1024 against 512: 105
+// against 87 at 1024, and at 512 a workgroup takes 90 where a wave takes 70).  Rows at odd
+// addresses are bound by their memory instructions, 8 (bf16) or 4 (fp32) for one that takes
+// 16 bytes: 62 against 43 us forward and 88 against 59 back at 1024.  Rows read twice are those that registers do not hold: at 2560 channels held ones take 59 against 104.
 struct Shape {
     int ch, threads;
     bool wave;
